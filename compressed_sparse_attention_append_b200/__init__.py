@@ -128,6 +128,7 @@ def lib():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
+        declare(L)
         _lib = L
     return _lib
 
@@ -414,3 +415,10 @@ def csa2_get_device_status(ws: Workspace, stream=None) -> int:
     if s not in (CSA2_OK, CSA2_ERR_DEVICE):
         raise Csa2Error("csa2_get_device_status", s)
     return v.value
+
+
+from .layer import (  # noqa: E402  (include/csa2_layer.h: the operators around the core)
+    CSA2_BF16, CSA2_DEV_BAD_PAGE, CSA2_F32, CSA2_ROPE_HALF, CSA2_ROPE_INTERLEAVED, LAYER_EXPORTS, PagedCache, Rope,
+    csa2_append_row, csa2_fp8_gemm, csa2_fp8_quantize, csa2_fp8_quantize_weight, csa2_heads, csa2_norm_rope,
+    csa2_paged_append, csa2_paged_attend, csa2_paged_cache, csa2_paged_gather, csa2_paged_index_topk, csa2_rope,
+    csa2_rope_frequencies, csa2_rope_spec, declare)

@@ -272,7 +272,7 @@ csa2_status csa2_latent_index_topk(const csa2_latent_cache* cache, int batch, in
     a.qpos = qpos;
     a.flags = flags;
     a.out_idx = out_idx;
-    return from_cuda(launch_latent_index(a, idx_q, reinterpret_cast<unsigned char*>(ws), (cudaStream_t)stream));
+    return from_cuda(launch_latent_index(a, false, idx_q, reinterpret_cast<unsigned char*>(ws), (cudaStream_t)stream));
 }
 
 const char* csa2_status_string(csa2_status s) {

@@ -14,6 +14,7 @@
 #include <stdint.h>
 
 #include "../../include/csa2.h"
+#include "../../include/csa2_layer.h"
 
 namespace csa2 {
 
@@ -502,8 +503,29 @@ struct LatentAppendArgs {
 };
 cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t s);
 
+// Where the entries and the window rings of a paged latent cache are (include/csa2_layer.h,
+// csa2_paged_cache); the planes' pointers travel in a csa2_latent_cache whose cap is max_pages << shift.
+struct PageMap {
+    const int32_t* table;     // [sequences][max_pages]
+    const int32_t* swa_slot;  // [sequences] or NULL: the sequence's number
+    int64_t n_pages, max_pages, n_slots;
+    int shift;                // log2 of the entries per page
+};
+// Plane row of entry p (0 <= p < max_pages << shift) of sequence b, or -1: its page is not there.
+__device__ __forceinline__ int64_t paged_row(const PageMap& m, int b, int64_t p) {
+    const int32_t page = __ldg(m.table + (int64_t)b * m.max_pages + (p >> m.shift));
+    if (page < 0 || page >= m.n_pages) return -1;
+    return ((int64_t)page << m.shift) + (p & ((1 << m.shift) - 1));
+}
+// Window ring of sequence b, or -1: it is not there.
+__device__ __forceinline__ int64_t paged_slot(const PageMap& m, int b) {
+    const int64_t s = m.swa_slot ? __ldg(m.swa_slot + b) : b;
+    return s < 0 || s >= m.n_slots ? -1 : s;
+}
+
 struct LatentAttendArgs {
     csa2_latent_cache c;
+    PageMap pg;                // paged launches
     int rows, tq, k, win, ratio;
     const int64_t* qpos;       // [rows]
     const int64_t* swa_begin;  // [rows / tq] or NULL
@@ -517,10 +539,12 @@ struct LatentAttendArgs {
 };
 size_t latent_attend_smem_bytes();
 cudaError_t launch_latent_attend(const LatentAttendArgs& a, cudaStream_t s);
+cudaError_t launch_paged_attend(const LatentAttendArgs& a, cudaStream_t s);  // over the pages of a.pg
 
 constexpr int kLatMaxHI = 64;    // indexer query heads the latent indexer takes
 struct LatIndexArgs {
     csa2_latent_cache c;
+    PageMap pg;                   // paged launches
     int rows, tq, hi, k, ratio;
     int64_t max_ctx;              // bound on a row's visible entries (the key buffer's row length)
     const int64_t* qpos;          // [rows]
@@ -533,6 +557,7 @@ struct LatIndexArgs {
     uint32_t* status;
 };
 size_t latent_index_ws_bytes(int rows, int hi, int64_t max_ctx);
-cudaError_t launch_latent_index(LatIndexArgs a, const uint16_t* idx_q, unsigned char* ws, cudaStream_t s);
+// paged: over the pages of a.pg
+cudaError_t launch_latent_index(LatIndexArgs a, bool paged, const uint16_t* idx_q, unsigned char* ws, cudaStream_t s);
 
 }  // namespace csa2

@@ -1,0 +1,410 @@
+// fp8.cu -- products in E4M3 with one scale per 128 channels of a row and per 128 x 128 block of the
+// weights, and the two quantisers that write those formats (csa2_fp8_quantize,
+// csa2_fp8_quantize_weight, csa2_fp8_gemm).
+//
+//   out[i][j] = sum_b xs[b][i] ws[j / 128][b] sum_{c in block b} x[i][c] w[j][c]
+//
+// A block's sum (128 exact products) comes from tcgen05 (kind::f8f6f4) in fp32 tensor memory; the
+// scales differ per row and block, so each block's sum is read back, scaled and added to the tile's
+// sums in fp32 registers while the tensor cores form the next block's.
+#include <mutex>
+
+#include "csa2_internal.cuh"
+#include "csa2_layer.cuh"
+#include "tc.cuh"
+
+namespace csa2 {
+
+namespace {
+
+using namespace tc;
+
+constexpr float kE4M3Max = 448.f;
+
+// ---- quantisers --------------------------------------------------------------------------------------
+
+__device__ __forceinline__ void load8_bf16(const uint16_t* p, float (&x)[8]) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+// the larger one, NaN when either is (a NaN is not lost in a block's maximum)
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float amax8(const float (&x)[8]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
+    return m;
+}
+// the codes of x / s (fp32 quotients; s == 0: +0)
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float s) {
+    uint32_t c[4] = {0u, 0u, 0u, 0u};
+    if (s != 0.f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = f32x2_to_e4m3x2(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s));
+    }
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// 16 lanes per (row, block of 128), 16 rows per CTA, U blocks per lane group: all loads first.
+template <int U>
+__global__ void __launch_bounds__(256) fp8_rows_kernel(int64_t rows, int k, const uint16_t* x, int64_t x_stride,
+                                                       uint8_t* data, float* scale) {
+    const int l = threadIdx.x & 15, nb = (k + 127) / 128, b0 = blockIdx.y * U;
+    const int64_t r = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    wait_prior_grid();
+    float v[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = (b0 + u) * 128 + l * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+        if (r < rows && c < k) load8_bf16(x + r * x_stride + c, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float m = amax8(v[u]);
+        for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float s = __fdiv_rn(m, kE4M3Max);
+        const int c = (b0 + u) * 128 + l * 8;
+        if (r < rows && c < k) *reinterpret_cast<uint2*>(data + r * k + c) = codes8(v[u], s);
+        if (r < rows && l == 0 && b0 + u < nb) scale[(int64_t)(b0 + u) * rows + r] = s;
+    }
+}
+
+// One CTA per 128 x 128 block: 16 rows of 16 lanes at a time, eight times.
+__global__ void __launch_bounds__(256) fp8_weight_kernel(int64_t n, int k, const uint16_t* w, uint8_t* data,
+                                                         float* scale) {
+    __shared__ float red[8];
+    const int c = blockIdx.x * 128 + (threadIdx.x & 15) * 8;
+    const int64_t r0 = (int64_t)blockIdx.y * 128 + (threadIdx.x >> 4);
+    wait_prior_grid();
+    float v[8][8], m = 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        const int64_t r = r0 + 16 * u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+        if (r < n && c < k) load8_bf16(w + r * k + c, v[u]);
+        m = max_nan(m, amax8(v[u]));
+    }
+    for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (!(threadIdx.x & 31)) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = red[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max_nan(m, red[i]);
+    const float s = __fdiv_rn(m, kE4M3Max);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        const int64_t r = r0 + 16 * u;
+        if (r < n && c < k) *reinterpret_cast<uint2*>(data + r * k + c) = codes8(v[u], s);
+    }
+    if (threadIdx.x == 0) scale[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
+}
+
+// ---- the product ---------------------------------------------------------------------------------------
+
+constexpr uint64_t kWaitNs = 200000000ull;
+
+// D[tmem] (+)= A B^T, E4M3 x E4M3 -> fp32, both K-major; K = 32 per instruction. Issued by one thread.
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+__host__ __device__ constexpr uint32_t f8_idesc(int m, int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// a float of CTA `rank`'s shared memory, at the address that `addr` has in this CTA's
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+                 : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void store_out(const Fp8GemmArgs& a, int64_t i, int64_t j, float v) {
+    if (a.out_f32)
+        reinterpret_cast<float*>(a.out)[i * a.out_stride + j] = v;
+    else
+        reinterpret_cast<uint16_t*>(a.out)[i * a.out_stride + j] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// Tiles of 128 weight rows (the MMA's M: a lane of tensor memory per output column) x NT rows of x.
+// The weights' scale of a block is then one number per tile, the rows' scales are along the
+// registers of a thread. Warp 0 copies, warp 1 issues the MMAs, warps 2 .. 5 scale and add. The
+// blocks of the contraction are split over the a cluster's CTAs; their sums meet in shared memory and
+// are added in rank order.
+template <int NT>
+struct Cols {
+    static constexpr int kThreads = 192;
+    static constexpr int kStage = 128 * 128 + NT * 128;
+    static constexpr int kStages = NT <= 32 ? 5 : (NT == 64 ? 4 : 3);
+    static constexpr uint32_t kTmem = 2 * NT < 32 ? 32 : 2 * NT;  // two accumulators
+    static constexpr int kJoin = NT * 128 * 4;                    // this CTA's sums for the join
+    static constexpr int kData = kStages * kStage > kJoin ? kStages * kStage : kJoin;
+    static constexpr int kSmem = kData + 2 * NT * 4 + (2 * kStages + 4) * 8 + 16 + 1024;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(192) fp8_cols_kernel(Fp8GemmArgs a, const __grid_constant__ CUtensorMap wmap,
+                                                       const __grid_constant__ CUtensorMap xmap, int split) {
+    using G = Cols<NT>;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float* sc = reinterpret_cast<float*>(sm + G::kData);  // [2][NT]: the rows' scales of a block
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + G::kData + 2 * NT * 4);
+    uint64_t* empty = full + G::kStages;
+    uint64_t* tfull = empty + G::kStages;
+    uint64_t* tempty = tfull + 2;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(tempty + 2);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = split > 1 ? (int)cluster_rank() : 0;
+    const int64_t tile = blockIdx.x / (unsigned)split, mt = (a.m + NT - 1) / NT;
+    const int64_t m0 = tile % mt * NT, n0 = tile / mt * 128;
+    const int nb = (a.k + 127) / 128;
+    const int b0 = (int)((int64_t)nb * rank / split), b1 = (int)((int64_t)nb * (rank + 1) / split);
+
+    if (tid == 0) {
+        for (int i = 0; i < G::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 128);
+        }
+        mbar_fence_init();
+        prefetch_tmap(&wmap);
+        prefetch_tmap(&xmap);
+    }
+    if (warp == 1) tmem_alloc(slot, G::kTmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = *slot;
+    wait_prior_grid();
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !mbar_wait(bar, parity, kWaitNs)) {
+            ok = false;
+            set_status(a.status, CSA2_DEV_TIMEOUT);
+        }
+        return ok;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int issued = 0;
+            for (int b = b0, i = 0; b < b1; ++b, ++i) {
+                const int st = i % G::kStages;
+                if (i >= G::kStages && !wait(&empty[st], ((i / G::kStages) - 1) & 1)) break;
+                unsigned char* d = sm + st * G::kStage;
+                mbar_expect_tx(&full[st], G::kStage);
+                tma_2d_g2s(d, &wmap, b * 128, (int)n0, &full[st]);
+                tma_2d_g2s(d + 128 * 128, &xmap, b * 128, (int)m0, &full[st]);
+                issued = i + 1;
+            }
+            // no copy is in flight when the CTA ends, even when a wait ran out (bounded again)
+            for (int i = issued > G::kStages ? issued - G::kStages : 0; i < issued; ++i)
+                mbar_wait(&full[i % G::kStages], (i / G::kStages) & 1, kWaitNs);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            for (int b = b0, i = 0; b < b1; ++b, ++i) {
+                const int st = i % G::kStages, buf = i & 1;
+                if (i >= 2 && !wait(&tempty[buf], ((i >> 1) - 1) & 1)) break;
+                if (!wait(&full[st], (i / G::kStages) & 1)) break;
+                tc_fence_after();
+                const uint32_t ad = smem_u32(sm + st * G::kStage), bd = ad + 128 * 128;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    mma_f8(tb + buf * NT, sw128_desc(ad + 32 * q), sw128_desc(bd + 32 * q), f8_idesc(128, NT), q > 0);
+                mma_commit(&empty[st]);
+                mma_commit(&tfull[buf]);
+            }
+        }
+        __syncwarp();
+    } else {
+        const int et = tid - 64;        // 0 .. 127
+        const int quad = warp & 3;      // the tensor-memory lanes this warp may read
+        const int64_t row = m0 + et;    // the row of x whose scales this thread fetches
+        float acc[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[i] = 0.f;
+        auto fetch = [&](int b) {
+            return (b < b1 && et < NT && row < a.m)
+                       ? __ldg(a.xs + (int64_t)b * a.m + row) * __ldg(a.ws + (n0 >> 7) * nb + b) : 0.f;
+        };
+        float s0 = fetch(b0), s1 = fetch(b0 + 1);
+        for (int b = b0, i = 0; b < b1; ++b, ++i) {
+            const int buf = i & 1;
+            if (et < NT) sc[buf * NT + et] = s0;
+            s0 = s1;
+            s1 = fetch(b + 2);
+            wait(&tfull[buf], (i >> 1) & 1);
+            asm volatile("bar.sync 1, 128;" ::: "memory");  // the scales of block b (and b - 1 is read)
+            tc_fence_after();
+            constexpr int W = NT < 32 ? 16 : 32;
+#pragma unroll
+            for (int c = 0; c < NT; c += W) {
+                uint32_t v[W];
+                const uint32_t at = tb + ((uint32_t)(32 * quad) << 16) + buf * NT + c;
+                if constexpr (W == 32) tmem_ld32(at, v); else tmem_ld16(at, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < W; j += 4) {
+                    const float4 s = *reinterpret_cast<const float4*>(sc + buf * NT + c + j);
+                    acc[c + j] = fmaf(__uint_as_float(v[j]), s.x, acc[c + j]);
+                    acc[c + j + 1] = fmaf(__uint_as_float(v[j + 1]), s.y, acc[c + j + 1]);
+                    acc[c + j + 2] = fmaf(__uint_as_float(v[j + 2]), s.z, acc[c + j + 2]);
+                    acc[c + j + 3] = fmaf(__uint_as_float(v[j + 3]), s.w, acc[c + j + 3]);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&tempty[buf]);
+        }
+        const int n = 32 * quad + lane;
+        if (split == 1) {
+            if (n0 + n < a.n) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    if (m0 + i < a.m) store_out(a, m0 + i, n0 + n, acc[i]);
+            }
+        } else {
+            // every copy of this CTA has landed and been read: the stages become the sums [NT][128]
+            float* part = reinterpret_cast<float*>(sm);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) part[i * 128 + n] = acc[i];
+        }
+    }
+    if (split > 1) {
+        __syncwarp();
+        cluster_sync();
+        const int i0 = NT * rank / split, i1 = NT * (rank + 1) / split;
+        for (int e = tid + i0 * 128; e < i1 * 128; e += G::kThreads) {
+            const int i = e >> 7, n = e & 127;
+            if (m0 + i >= a.m || n0 + n >= a.n) continue;
+            float v = 0.f;
+            for (int r = 0; r < split; ++r) v += ld_cluster(smem_u32(sm) + 4u * e, r);
+            store_out(a, m0 + i, n0 + n, v);
+        }
+        cluster_sync();  // the peers have read this CTA's sums
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tb, G::kTmem);
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+    static std::once_flag once;
+    static EncodeTiledFn fn = nullptr;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// rows x k bytes, boxes of box_rows x 128 in the 128-byte swizzle; past the edges zeros are read
+cudaError_t make_map(CUtensorMap* map, const uint8_t* p, int64_t rows, int k, int box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dim[2] = {(cuuint64_t)k, (cuuint64_t)rows}, str[1] = {(cuuint64_t)k};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows}, es[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dim, str, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int NT>
+cudaError_t launch_cols(const Fp8GemmArgs& a, cudaStream_t s) {
+    using G = Cols<NT>;
+    auto k = fp8_cols_kernel<NT>;
+    CUtensorMap wmap, xmap;
+    cudaError_t e = make_map(&wmap, a.w, a.n, a.k, 128);
+    if (e == cudaSuccess) e = make_map(&xmap, a.x, a.m, a.k, NT);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = ((a.n + 127) / 128) * ((a.m + NT - 1) / NT);
+    const int nb = (a.k + 127) / 128;
+    // the contraction split (by 2, 4 or 8) while that still gives about one CTA per SM, two blocks each
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= 160 && nb >= split * 4) split *= 2;
+    if (tiles * split > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * split));
+    cfg.blockDim = dim3(G::kThreads);
+    cfg.dynamicSmemBytes = G::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k, a, wmap, xmap, split);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_rows(int64_t rows, int k, const uint16_t* x, int64_t x_stride, uint8_t* data, float* scale,
+                            cudaStream_t s) {
+    const int nb = (k + 127) / 128;
+    const int64_t gx = (rows + 15) / 16;
+    if (gx > 0x7FFFFFFF || nb > 65535) return cudaErrorInvalidConfiguration;
+    // several blocks per lane group once they fill the GPU (eight CTAs an SM)
+    if (gx * nb >= 148 * 8 * 4)
+        return launch_after_prior(fp8_rows_kernel<4>, dim3((unsigned)gx, (unsigned)((nb + 3) / 4)), dim3(256), 0, s,
+                                  rows, k, x, x_stride, data, scale);
+    return launch_after_prior(fp8_rows_kernel<1>, dim3((unsigned)gx, (unsigned)nb), dim3(256), 0, s, rows, k, x,
+                              x_stride, data, scale);
+}
+
+cudaError_t launch_fp8_weight(int64_t n, int k, const uint16_t* w, uint8_t* data, float* scale, cudaStream_t s) {
+    const int64_t gy = (n + 127) / 128;
+    if (gy > 65535) return cudaErrorInvalidConfiguration;
+    return launch_after_prior(fp8_weight_kernel, dim3((unsigned)((k + 127) / 128), (unsigned)gy), dim3(256), 0, s, n, k,
+                              w, data, scale);
+}
+
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t s) {
+    if (a.m <= 16) return launch_cols<16>(a, s);
+    if (a.m <= 32) return launch_cols<32>(a, s);
+    if (a.m <= 64) return launch_cols<64>(a, s);
+    return launch_cols<128>(a, s);
+}
+
+}  // namespace csa2

@@ -123,6 +123,9 @@ __device__ __forceinline__ float warp_sum16(float (&v)[16], int lane) {
     return v[0];
 }
 
+// PAGED: the entries and window rings are those of a paged cache (a.pg); the row's indices are
+// translated to plane rows while they are staged, once per row.
+template <bool PAGED>
 __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -154,7 +157,10 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
         if (lo < sb) lo = sb;
         if (lo < 0) lo = 0;
     }
-    const int nwin = (row_ok && qpos >= lo) ? (int)(qpos - lo + 1) : 0;
+    int64_t ring = b;  // the window ring of this row
+    if constexpr (PAGED) ring = a.win > 0 ? paged_slot(a.pg, b) : -1;
+    if (PAGED && ring < 0 && a.win > 0 && threadIdx.x == 0) set_status(a.status, CSA2_DEV_BAD_PAGE);
+    const int nwin = (row_ok && qpos >= lo && (!PAGED || ring >= 0)) ? (int)(qpos - lo + 1) : 0;
     const int ft = row_ok ? (K + kTile - 1) / kTile : 0;
     const int nt = ft + (nwin > 0 ? 1 : 0);
     const float scale2 = a.sm_scale * 1.4426950408889634f;  // logits in log2 units
@@ -183,11 +189,17 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
         const int v = __ldg(a.idx + (size_t)row * K + i);
         const bool ok = v >= 0 && (int64_t)v <= qlast && (int64_t)v < a.c.cap;
         if (!ok && v != -1) set_status(status, CSA2_DEV_BAD_INDEX);
-        sidx[i] = ok ? v : -1;
+        if constexpr (PAGED) {
+            const int64_t at = ok ? paged_row(a.pg, b, v) : -1;  // a plane row (below 2^31)
+            if (ok && at < 0) set_status(status, CSA2_DEV_BAD_PAGE);
+            sidx[i] = (int)at;
+        } else {
+            sidx[i] = ok ? v : -1;
+        }
     }
 
-    const size_t seq_row0 = (size_t)b * a.c.cap;
-    const size_t swa_row0 = (size_t)b * a.c.swa_cap;
+    const size_t seq_row0 = PAGED ? 0 : (size_t)b * a.c.cap;
+    const size_t swa_row0 = (size_t)(PAGED ? ring : (int64_t)b) * a.c.swa_cap;
     bool ok_all = true;
     auto wait_bar = [&](int i, uint32_t parity) {
         if (!mbar_wait(&bars[i], parity, kWaitNs)) {
@@ -459,11 +471,16 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
 
 size_t latent_attend_smem_bytes() { return kSmem; }
 
-cudaError_t launch_latent_attend(const LatentAttendArgs& a, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(latent_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+template <bool PAGED>
+static cudaError_t launch_rows(const LatentAttendArgs& a, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(latent_attend_kernel<PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmem);
     if (e != cudaSuccess) return e;
     if (a.rows == 0) return cudaSuccess;
-    return launch_after_prior(latent_attend_kernel, dim3((unsigned)a.rows), dim3(kT), kSmem, s, a);
+    return launch_after_prior(latent_attend_kernel<PAGED>, dim3((unsigned)a.rows), dim3(kT), kSmem, s, a);
 }
+
+cudaError_t launch_latent_attend(const LatentAttendArgs& a, cudaStream_t s) { return launch_rows<false>(a, s); }
+cudaError_t launch_paged_attend(const LatentAttendArgs& a, cudaStream_t s) { return launch_rows<true>(a, s); }
 
 }  // namespace csa2

@@ -19,6 +19,8 @@
 // covers the workloads by a wide margin. The scores then are the exact rational scores (times 4),
 // and so is the ranking.
 //
+// Over a paged cache (PAGED) an entry's plane row comes from the page table; all else is the same.
+//
 // lat_index_score_kernel: one thread per (row, visible position); the row's quantised query sits
 //   in shared memory as int8 words and fp64 block scales; the position's 64 code bytes become 32
 //   int8 words in registers. Writes the orderable 64-bit key of each score.
@@ -65,6 +67,7 @@ __device__ __forceinline__ int64_t lat_visible(const LatIndexArgs& a, int row) {
     return n;
 }
 
+template <bool PAGED>
 __global__ void __launch_bounds__(kSThr) lat_index_score_kernel(LatIndexArgs a) {
     __shared__ uint32_t qw[kLatMaxHI][32];  // twice the quantised query, int8 x 4 per word
     __shared__ double qs[kLatMaxHI][4];     // its block scales
@@ -89,7 +92,16 @@ __global__ void __launch_bounds__(kSThr) lat_index_score_kernel(LatIndexArgs a) 
     const int64_t p = (int64_t)blockIdx.x * kSThr + tid;
     if (p >= n) return;
     const int b = row / a.tq;
-    const size_t e = (size_t)b * a.c.cap + (size_t)p;
+    size_t e = (size_t)b * a.c.cap + (size_t)p;
+    if constexpr (PAGED) {
+        const int64_t at = paged_row(a.pg, b, p);
+        if (at < 0) {  // its page is not there: below every score
+            set_status(a.status, CSA2_DEV_BAD_PAGE);
+            a.keys[(size_t)row * a.key_stride + p] = 0ull;
+            return;
+        }
+        e = (size_t)at;
+    }
     uint32_t kw[32];
     {
         const uint4* src = reinterpret_cast<const uint4*>(a.c.k_data + e * kLatKBytes);
@@ -219,7 +231,7 @@ size_t latent_index_ws_bytes(int rows, int hi, int64_t max_ctx) {
     return off;
 }
 
-cudaError_t launch_latent_index(LatIndexArgs a, const uint16_t* idx_q, unsigned char* ws, cudaStream_t s) {
+cudaError_t launch_latent_index(LatIndexArgs a, bool paged, const uint16_t* idx_q, unsigned char* ws, cudaStream_t s) {
     size_t off = 256;
     a.status = reinterpret_cast<uint32_t*>(ws);
     uint8_t* qcodes = ws + off;
@@ -234,7 +246,9 @@ cudaError_t launch_latent_index(LatIndexArgs a, const uint16_t* idx_q, unsigned 
     cudaError_t e = launch_mxfp4(idx_q, (long long)a.rows * a.hi, 128, qcodes, qscales, s);
     if (e != cudaSuccess) return e;
     const long long bx = (a.max_ctx + kSThr - 1) / kSThr;
-    e = launch_after_prior(lat_index_score_kernel, dim3((unsigned)bx, (unsigned)a.rows), dim3(kSThr), 0, s, a);
+    const dim3 grid((unsigned)bx, (unsigned)a.rows);
+    e = paged ? launch_after_prior(lat_index_score_kernel<true>, grid, dim3(kSThr), 0, s, a)
+              : launch_after_prior(lat_index_score_kernel<false>, grid, dim3(kSThr), 0, s, a);
     if (e != cudaSuccess) return e;
     return launch_after_prior(lat_index_select_kernel, dim3((unsigned)a.rows), dim3(kQThr), 0, s, a);
 }

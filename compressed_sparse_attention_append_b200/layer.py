@@ -1,0 +1,278 @@
+"""Binding of include/csa2_layer.h: the operators around the CSA2 core. Argument marshalling only, in the
+manner of the package's other calls (same names as the C entry points, tensors for pointers, the
+current CUDA stream, Csa2Error on a non-zero status, no CPU fallback). Every tensor of a call lies on the
+current device.
+
+One decode step of a layer of the pages' own shape, `B` sequences (bf16 unless noted):
+
+    rope = Rope.for_context(64, 10000.0, "yarn", 16.0, 65536, offset=448, interleaved=True)
+    cache = PagedCache(n_pages, 64, B, max_pages)         # cache.table [B, max_pages] int32: the caller's
+    csa2_fp8_quantize(hidden, xq, xs)                      # E4M3 rows, one scale per 128 channels
+    csa2_fp8_gemm(xq, xs, wq, wq_scale, q.view(B, -1))     # ... one product per projection
+    csa2_norm_rope(rope, pos, eps, q, q_weight, q)         # per-head norm and rotation, in place
+    csa2_paged_append(cache, B, 1, pos, latent, idx_k, swa, rope=rope, idx_rope=idx_rope,
+                      w_latent=w_l, w_idx_k=w_k, w_swa=w_s, eps=eps, ws=ws)
+    csa2_paged_index_topk(cache, B, 1, pos, idx_q, 512, idx, index_ws)
+    csa2_paged_attend(cache, B, 1, pos, q, idx, 512, out, ws=ws)
+    csa2_rope(rope.transposed(), pos, out, out)            # K = V: the output turned back
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+CSA2_BF16 = 0
+CSA2_F32 = 1
+CSA2_DEV_BAD_PAGE = 0x10
+CSA2_ROPE_HALF = 0
+CSA2_ROPE_INTERLEAVED = 1
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+LAYER_EXPORTS = (
+    "csa2_rope_frequencies", "csa2_rope", "csa2_norm_rope", "csa2_fp8_quantize", "csa2_fp8_quantize_weight",
+    "csa2_fp8_gemm", "csa2_paged_append", "csa2_paged_gather", "csa2_paged_attend", "csa2_paged_index_topk",
+)
+
+
+class csa2_rope_spec(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot", ctypes.c_int), ("offset", ctypes.c_int),
+                ("layout", ctypes.c_int), ("transposed", ctypes.c_int), ("mscale", ctypes.c_float)]
+
+
+class csa2_heads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("x_token", ctypes.c_int64),
+                ("x_head", ctypes.c_int64), ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("heads", ctypes.c_int)]
+
+
+class csa2_append_row(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_batch", ctypes.c_int64), ("x_token", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("rope", ctypes.POINTER(csa2_rope_spec))]
+
+
+class csa2_paged_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("l_data", "l_scale", "k_data", "k_scale", "swa", "table", "swa_slot")]
+    _fields_ += [(n, ctypes.c_int64) for n in ("n_pages", "max_pages", "n_slots", "swa_cap")]
+    _fields_ += [("page", ctypes.c_int)]
+
+
+def declare(L):
+    """The signatures of include/csa2_layer.h on the loaded library."""
+    vp, i, i64, u32, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float, ctypes.c_size_t
+    dbl, P = ctypes.c_double, ctypes.POINTER
+    R, H, A, C = P(csa2_rope_spec), P(csa2_heads), P(csa2_append_row), P(csa2_paged_cache)
+    sig = {
+        "csa2_rope_frequencies": [i, dbl, i, dbl, i64, dbl, dbl, vp, P(f)],
+        "csa2_rope": [R, i, i64, i, vp, H, vp],
+        "csa2_norm_rope": [R, i, i64, i, vp, f, H, H, vp],
+        "csa2_fp8_quantize": [i64, i, vp, i64, vp, vp, vp],
+        "csa2_fp8_quantize_weight": [i64, i, vp, vp, vp, vp],
+        "csa2_fp8_gemm": [i64, i64, i, vp, vp, vp, vp, i, vp, i64, vp, sz, vp],
+        "csa2_paged_append": [C, i, i, vp, vp, vp, f, A, A, A, vp, sz, vp],
+        "csa2_paged_gather": [C, i, i, vp, vp, vp, vp, sz, vp],
+        "csa2_paged_attend": [C, i, i, vp, vp, vp, i, vp, i, i, f, vp, vp, vp, vp, sz, vp],
+        "csa2_paged_index_topk": [C, i, i, vp, vp, i, i, i, i64, u32, vp, vp, sz, vp],
+    }
+    for name, args in sig.items():
+        fn = getattr(L, name)
+        fn.restype = i
+        fn.argtypes = args
+
+
+from . import _check, _stream, lib  # noqa: E402  (the package imports this module last)
+
+_TYPES = {torch.bfloat16: CSA2_BF16, torch.float32: CSA2_F32}
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+_I64, _I32, _F32, _BF16, _U8 = (torch.int64,), (torch.int32,), (torch.float32,), (torch.bfloat16,), (torch.uint8,)
+
+
+def _ptr(t, dtypes, shape=None, dense=True):
+    """A tensor's pointer after the checks that the library cannot make (None stays None)."""
+    if t is None:
+        return None
+    assert isinstance(t, torch.Tensor) and t.dtype in dtypes, f"expected a {' or '.join(map(str, dtypes))} tensor"
+    assert t.is_cuda, "expected a CUDA tensor"
+    assert t.get_device() == torch.cuda.current_device(), "expected a tensor of the current device"
+    assert not dense or t.is_contiguous(), "expected a contiguous tensor"
+    assert shape is None or t.shape == shape, f"expected the shape {tuple(shape)}, got {tuple(t.shape)}"
+    return t.data_ptr()
+
+
+def _status(ws):
+    return (None, 0) if ws is None else (ws.ptr, ws.nbytes)
+
+
+class Rope:
+    """A rotation (csa2_rope_spec) and the tensor of its frequencies: inv_freq [rot / 2] float64, radians
+    per position; `offset` the first rotated channel; `inverse` turns back."""
+
+    def __init__(self, inv_freq, offset=0, interleaved=False, mscale=1.0, inverse=False):
+        self.inv_freq, self.offset, self.interleaved = inv_freq, int(offset), bool(interleaved)
+        self.mscale, self.inverse = float(mscale), bool(inverse)
+        self.rot = 2 * inv_freq.numel()
+        self.c = csa2_rope_spec(_ptr(inv_freq, (torch.float64,)), self.rot, self.offset, int(self.interleaved),
+                                int(self.inverse), self.mscale)
+        self.ref = ctypes.pointer(self.c)
+
+    @classmethod
+    def for_context(cls, rot, base=10000.0, scaling="plain", factor=1.0, orig_ctx=0, beta_fast=32.0, beta_slow=1.0,
+                    offset=0, interleaved=False, device="cuda"):
+        """The frequencies of csa2_rope_frequencies (scaling: "plain", "linear", "ntk" or "yarn")."""
+        f, mscale = csa2_rope_frequencies(rot, base, scaling, factor, orig_ctx, beta_fast, beta_slow)
+        return cls(f.to(device), offset, interleaved, mscale)
+
+    def transposed(self):
+        """The rotation back (times mscale again: the transposed matrix)."""
+        return Rope(self.inv_freq, self.offset, self.interleaved, self.mscale, not self.inverse)
+
+
+def csa2_rope_frequencies(rot, base=10000.0, scaling="plain", factor=1.0, orig_ctx=0, beta_fast=32.0, beta_slow=1.0):
+    """(inv_freq [rot / 2] float64 on the host, mscale)."""
+    f = torch.zeros(max(rot, 0) // 2, dtype=torch.float64)
+    m = ctypes.c_float(0.0)
+    _check("csa2_rope_frequencies", lib().csa2_rope_frequencies(
+        rot, base, ROPE_SCALINGS[scaling], factor, orig_ctx, beta_fast, beta_slow, f.data_ptr(), ctypes.byref(m)))
+    return f, m.value
+
+
+def _heads(x, out, weight, dtype, tokens, d):
+    assert x.dim() == 3 and x.shape[0] == tokens and x.shape[2] == d, "expected [tokens, heads, d]"
+    assert x.stride(2) == 1 and out.stride(2) == 1, "expected dense heads (stride 1 along the channels)"
+    xs, os = x.stride(), out.stride()
+    return csa2_heads(_ptr(x, dtype, dense=False), _ptr(out, dtype, x.shape, dense=False), xs[0], xs[1], os[0], os[1],
+                      _ptr(weight, dtype, (d,)), x.shape[1])
+
+
+def csa2_rope(rope: Rope, pos, x, out, stream=None):
+    """x [tokens, heads, d] bf16 or fp32 (any strides, dense heads) -> out (may be x), pos [tokens] int64."""
+    tokens, _, d = x.shape
+    assert x.dtype in _TYPES, "expected a bf16 or fp32 tensor"
+    h = _heads(x, out, None, (x.dtype,), tokens, d)
+    _check("csa2_rope", lib().csa2_rope(rope.ref, _TYPES[x.dtype], tokens, d, _ptr(pos, _I64, (tokens,)),
+                                        ctypes.byref(h), _stream(stream)))
+
+
+def csa2_norm_rope(rope, pos, eps, q, wq, q_out, k=None, wk=None, k_out=None, stream=None):
+    """q [tokens, hq, d] and k [tokens, hk, d] (or None) normed per head with weights wq, wk [d] (or None) and
+    rotated (rope None: the norm alone) -> q_out, k_out (may be q, k)."""
+    tokens, _, d = q.shape
+    assert q.dtype in _TYPES, "expected a bf16 or fp32 tensor"
+    hq = _heads(q, q_out, wq, (q.dtype,), tokens, d)
+    hk = _heads(k, k_out, wk, (q.dtype,), tokens, d) if k is not None else None
+    _check("csa2_norm_rope", lib().csa2_norm_rope(
+        rope.ref if rope is not None else None, _TYPES[q.dtype], tokens, d, _ptr(pos, _I64, (tokens,)), eps,
+        ctypes.byref(hq), ctypes.byref(hk) if hk is not None else None, _stream(stream)))
+
+
+def csa2_fp8_quantize(x, data, scale, stream=None):
+    """x [rows, k] bf16 (dense rows) -> data [rows, k] E4M3 (or uint8), scale [ceil(k / 128), rows] fp32."""
+    rows, k = x.shape
+    assert x.stride(1) == 1 or k == 1, "expected dense rows"
+    _check("csa2_fp8_quantize", lib().csa2_fp8_quantize(
+        rows, k, _ptr(x, _BF16, dense=False), x.stride(0), _ptr(data, _E4M3, x.shape),
+        _ptr(scale, _F32, (-(-k // 128), rows)), _stream(stream)))
+
+
+def csa2_fp8_quantize_weight(w, data, scale, stream=None):
+    """w [n, k] bf16 -> data [n, k] E4M3 (or uint8), scale [ceil(n / 128), ceil(k / 128)] fp32."""
+    n, k = w.shape
+    _check("csa2_fp8_quantize_weight", lib().csa2_fp8_quantize_weight(
+        n, k, _ptr(w, _BF16), _ptr(data, _E4M3, w.shape), _ptr(scale, _F32, (-(-n // 128), -(-k // 128))),
+        _stream(stream)))
+
+
+def csa2_fp8_gemm(x, xs, w, ws, out, status=None, stream=None):
+    """out [m, n] (bf16 or fp32, dense rows) = x [m, k] w [n, k]^T, E4M3 with the scales of csa2_fp8_quantize (xs)
+    and csa2_fp8_quantize_weight (ws); status: a workspace for CSA2_DEV_TIMEOUT."""
+    m, k = x.shape
+    n, nb = w.shape[0], -(-k // 128)
+    assert out.dtype in _TYPES, "expected a bf16 or fp32 tensor"
+    assert out.stride(1) == 1 or n == 1, "expected dense rows"
+    _check("csa2_fp8_gemm", lib().csa2_fp8_gemm(
+        m, n, k, _ptr(x, _E4M3), _ptr(xs, _F32, (nb, m)), _ptr(w, _E4M3, (n, k)), _ptr(ws, _F32, (-(-n // 128), nb)),
+        _TYPES[out.dtype], _ptr(out, (out.dtype,), (m, n), dense=False), max(out.stride(0), n), *_status(status),
+        _stream(stream)))
+
+
+class PagedCache:
+    """Planes of csa2_paged_cache, allocated with torch unless given: n_pages pages of `page` entries, the page
+    table of `batch` sequences ([batch, max_pages] int32, -1 = no page; the caller fills `table`) and
+    n_slots window rings (default: one per sequence; swa_slot [batch] int32 names each sequence's)."""
+
+    def __init__(self, n_pages, page, batch, max_pages, swa_cap=128, n_slots=None, swa_slot=None, device="cuda",
+                 latent=True, indexer=True, page_table=None, l_data=None, l_scale=None, k_data=None, k_scale=None,
+                 swa=None):
+        n_slots = batch if n_slots is None else n_slots
+        self.n_pages, self.page, self.batch, self.max_pages = n_pages, page, batch, max_pages
+        self.n_slots, self.swa_cap, self.swa_slot = n_slots, swa_cap, swa_slot
+        z = lambda t, *s: torch.zeros(*s, dtype=torch.uint8, device=device) if t is None else t
+        self.l_data = z(l_data, n_pages, page, 256) if latent else None
+        self.l_scale = z(l_scale, n_pages, page, 32) if latent else None
+        self.k_data = z(k_data, n_pages, page, 64) if indexer else None
+        self.k_scale = z(k_scale, n_pages, page, 4) if indexer else None
+        self.swa = z(swa, n_slots, swa_cap, 512)
+        self.table = page_table if page_table is not None else torch.full((batch, max_pages), -1, dtype=torch.int32,
+                                                                          device=device)
+        assert swa_slot is not None or n_slots >= batch, "expected a window ring per sequence"
+        self.c = csa2_paged_cache(
+            _ptr(self.l_data, _U8, (n_pages, page, 256)), _ptr(self.l_scale, _U8, (n_pages, page, 32)),
+            _ptr(self.k_data, _U8, (n_pages, page, 64)), _ptr(self.k_scale, _U8, (n_pages, page, 4)),
+            _ptr(self.swa, _U8, (n_slots, swa_cap, 512)), _ptr(self.table, _I32, (batch, max_pages)),
+            _ptr(swa_slot, _I32, (batch,)), n_pages, max_pages, n_slots, swa_cap, page)
+        self.ref = ctypes.byref(self.c)
+
+
+def _append_row(x, weight, rope, batch, t, channels):
+    if x is None:
+        return None
+    assert x.shape == (batch, t, channels) and x.stride(2) == 1, f"expected dense rows [{batch}, {t}, {channels}]"
+    return ctypes.byref(csa2_append_row(_ptr(x, _BF16, dense=False), x.stride(0), x.stride(1),
+                                        _ptr(weight, _BF16, (channels,)), rope.ref if rope is not None else None))
+
+
+def csa2_paged_append(cache: PagedCache, batch, t, pos, latent=None, idx_k=None, swa=None, rope=None, idx_rope=None,
+                      swa_rope=None, w_latent=None, w_idx_k=None, w_swa=None, eps=1e-6, length=None, rpos=None,
+                      ws=None, stream=None):
+    """latent [B, t, 512], idx_k [B, t, 128], swa [B, t, 512] bf16 (any may be None; any strides, dense rows) at
+    entries pos [B] int64, normed with the weights that are given and rotated (`rope` latent and window rows,
+    unless swa_rope is given, `idx_rope` the key); length [B] int32: tokens of each sequence (None: t);
+    rpos [B, t] int64: the tokens' positions for the rotation (None: those of the entries)."""
+    assert batch <= cache.batch, "expected at most the page table's sequences"
+    _check("csa2_paged_append", lib().csa2_paged_append(
+        cache.ref, batch, t, _ptr(pos, _I64, (batch,)), _ptr(length, _I32, (batch,)), _ptr(rpos, _I64, (batch, t)), eps,
+        _append_row(latent, w_latent, rope, batch, t, 512), _append_row(idx_k, w_idx_k, idx_rope, batch, t, 128),
+        _append_row(swa, w_swa, swa_rope if swa_rope is not None else rope, batch, t, 512), *_status(ws),
+        _stream(stream)))
+
+
+def csa2_paged_gather(cache: PagedCache, batch, idx, latent=None, key=None, ws=None, stream=None):
+    """idx [B, n] int32 entries (-1: zeros) -> latent [B, n, 512] and key [B, n, 128] bf16 (either may be None)."""
+    assert batch <= cache.batch, "expected at most the page table's sequences"
+    n = idx.shape[1]
+    _check("csa2_paged_gather", lib().csa2_paged_gather(
+        cache.ref, batch, n, _ptr(idx, _I32, (batch, n)), _ptr(latent, _BF16, (batch, n, 512)),
+        _ptr(key, _BF16, (batch, n, 128)), *_status(ws), _stream(stream)))
+
+
+def csa2_paged_attend(cache: PagedCache, batch, tq, qpos, q, idx, k, out, swa_begin=None, win=128, ratio=1,
+                      sm_scale=0.0, out_f32=None, lse=None, ws=None, stream=None):
+    """q [B*tq, 64, 512] bf16, idx [B*tq, k] int32 -> out [B*tq, 64, 512] bf16 (tensor cores)."""
+    assert batch <= cache.batch, "expected at most the page table's sequences"
+    rows = batch * tq
+    _check("csa2_paged_attend", lib().csa2_paged_attend(
+        cache.ref, batch, tq, _ptr(qpos, _I64, (rows,)), _ptr(q, _BF16, (rows, 64, 512)), _ptr(idx, _I32), k,
+        _ptr(swa_begin, _I64, (batch,)), win, ratio, sm_scale, _ptr(out, _BF16, (rows, 64, 512)),
+        _ptr(out_f32, _F32, (rows, 64, 512)), _ptr(lse, _F32, (rows, 64)), *_status(ws), _stream(stream)))
+
+
+def csa2_paged_index_topk(cache: PagedCache, batch, tq, qpos, idx_q, k, out_idx, ws, ratio=1, max_ctx=None, flags=0,
+                          stream=None):
+    """idx_q [B*tq, hi, 128] bf16 -> out_idx [B*tq, k] int32; ws: a LatentIndexWorkspace."""
+    assert batch <= cache.batch, "expected at most the page table's sequences"
+    rows = batch * tq
+    if max_ctx is None:
+        max_ctx = cache.max_pages * cache.page
+    _check("csa2_paged_index_topk", lib().csa2_paged_index_topk(
+        cache.ref, batch, tq, _ptr(qpos, _I64, (rows,)), _ptr(idx_q, _BF16, (rows, idx_q.shape[-2], 128)),
+        idx_q.shape[-2], k, ratio, max_ctx, flags, _ptr(out_idx, _I32, (rows, k)), *_status(ws), _stream(stream)))
