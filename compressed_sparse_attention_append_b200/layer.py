@@ -80,23 +80,52 @@ def declare(L):
         fn.argtypes = args
 
 
-from . import _check, _stream, lib  # noqa: E402  (the package imports this module last)
+from . import Csa2Error, _check, lib  # noqa: E402  (the package imports this module last)
 
 _TYPES = {torch.bfloat16: CSA2_BF16, torch.float32: CSA2_F32}
-_E4M3 = (torch.float8_e4m3fn, torch.uint8)
-_I64, _I32, _F32, _BF16, _U8 = (torch.int64,), (torch.int32,), (torch.float32,), (torch.bfloat16,), (torch.uint8,)
+_I64, _I32, _F32, _BF16, _U8, _F64 = torch.int64, torch.int32, torch.float32, torch.bfloat16, torch.uint8, torch.float64
+_E4M3 = torch.float8_e4m3fn  # (uint8 bytes are taken too)
+_raw_device = None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _ptr(t, dtypes, shape=None, dense=True):
-    """A tensor's pointer after the checks that the library cannot make (None stays None)."""
-    if t is None:
-        return None
-    assert isinstance(t, torch.Tensor) and t.dtype in dtypes, f"expected a {' or '.join(map(str, dtypes))} tensor"
+def _device():
+    """The current device (-2 without a GPU, which no tensor lies on)."""
+    global _raw_device
+    if _raw_device is None:
+        if not torch.cuda.is_available():
+            return -2
+        torch.cuda.init()
+        _raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _raw_device()
+
+
+def _stream(stream, dev):
+    """The stream's handle; the current one's through the short way (a decode step's calls are host time)."""
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _refuse(t, dtype, dev, shape, dense):
+    """Names what is wrong with a tensor that _ptr did not take."""
+    names = f"{dtype} or {_U8}" if dtype is _E4M3 else str(dtype)
+    assert isinstance(t, torch.Tensor) and (t.dtype is dtype or (dtype is _E4M3 and t.dtype is _U8)), f"expected a {names} tensor"
     assert t.is_cuda, "expected a CUDA tensor"
-    assert t.get_device() == torch.cuda.current_device(), "expected a tensor of the current device"
+    assert t.get_device() == dev, "expected a tensor of the current device"
     assert not dense or t.is_contiguous(), "expected a contiguous tensor"
     assert shape is None or t.shape == shape, f"expected the shape {tuple(shape)}, got {tuple(t.shape)}"
     return t.data_ptr()
+
+
+def _ptr(t, dtype, dev, shape=None, dense=True):
+    """A tensor's pointer after the checks that the library cannot make (None stays None)."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and (not dense or t.is_contiguous()) \
+            and (shape is None or t.shape == shape):
+        return t.data_ptr()
+    return _refuse(t, dtype, dev, shape, dense)
 
 
 def _status(ws):
@@ -111,7 +140,7 @@ class Rope:
         self.inv_freq, self.offset, self.interleaved = inv_freq, int(offset), bool(interleaved)
         self.mscale, self.inverse = float(mscale), bool(inverse)
         self.rot = 2 * inv_freq.numel()
-        self.c = csa2_rope_spec(_ptr(inv_freq, (torch.float64,)), self.rot, self.offset, int(self.interleaved),
+        self.c = csa2_rope_spec(_ptr(inv_freq, _F64, _device()), self.rot, self.offset, int(self.interleaved),
                                 int(self.inverse), self.mscale)
         self.ref = ctypes.pointer(self.c)
 
@@ -136,63 +165,77 @@ def csa2_rope_frequencies(rot, base=10000.0, scaling="plain", factor=1.0, orig_c
     return f, m.value
 
 
-def _heads(x, out, weight, dtype, tokens, d):
-    assert x.dim() == 3 and x.shape[0] == tokens and x.shape[2] == d, "expected [tokens, heads, d]"
-    assert x.stride(2) == 1 and out.stride(2) == 1, "expected dense heads (stride 1 along the channels)"
-    xs, os = x.stride(), out.stride()
-    return csa2_heads(_ptr(x, dtype, dense=False), _ptr(out, dtype, x.shape, dense=False), xs[0], xs[1], os[0], os[1],
-                      _ptr(weight, dtype, (d,)), x.shape[1])
+def _heads(x, out, weight, dtype, dev, tokens, d):
+    t, heads, ch = x.shape
+    x0, x1, x2 = x.stride()
+    o0, o1, o2 = out.stride()
+    assert t == tokens and ch == d, "expected [tokens, heads, d]"
+    assert x2 == 1 and o2 == 1, "expected dense heads (stride 1 along the channels)"
+    return csa2_heads(_ptr(x, dtype, dev, None, False), _ptr(out, dtype, dev, x.shape, False), x0, x1, o0, o1,
+                      None if weight is None else _ptr(weight, dtype, dev, (d,)), heads)
 
 
 def csa2_rope(rope: Rope, pos, x, out, stream=None):
     """x [tokens, heads, d] bf16 or fp32 (any strides, dense heads) -> out (may be x), pos [tokens] int64."""
     tokens, _, d = x.shape
-    assert x.dtype in _TYPES, "expected a bf16 or fp32 tensor"
-    h = _heads(x, out, None, (x.dtype,), tokens, d)
-    _check("csa2_rope", lib().csa2_rope(rope.ref, _TYPES[x.dtype], tokens, d, _ptr(pos, _I64, (tokens,)),
-                                        ctypes.byref(h), _stream(stream)))
+    dtype, dev = x.dtype, _device()
+    assert dtype in _TYPES, "expected a bf16 or fp32 tensor"
+    h = _heads(x, out, None, dtype, dev, tokens, d)
+    s = lib().csa2_rope(rope.ref, _TYPES[dtype], tokens, d, _ptr(pos, _I64, dev, (tokens,)), ctypes.byref(h),
+                        _stream(stream, dev))
+    if s:
+        raise Csa2Error("csa2_rope", s)
 
 
 def csa2_norm_rope(rope, pos, eps, q, wq, q_out, k=None, wk=None, k_out=None, stream=None):
     """q [tokens, hq, d] and k [tokens, hk, d] (or None) normed per head with weights wq, wk [d] (or None) and
     rotated (rope None: the norm alone) -> q_out, k_out (may be q, k)."""
     tokens, _, d = q.shape
-    assert q.dtype in _TYPES, "expected a bf16 or fp32 tensor"
-    hq = _heads(q, q_out, wq, (q.dtype,), tokens, d)
-    hk = _heads(k, k_out, wk, (q.dtype,), tokens, d) if k is not None else None
-    _check("csa2_norm_rope", lib().csa2_norm_rope(
-        rope.ref if rope is not None else None, _TYPES[q.dtype], tokens, d, _ptr(pos, _I64, (tokens,)), eps,
-        ctypes.byref(hq), ctypes.byref(hk) if hk is not None else None, _stream(stream)))
+    dtype, dev = q.dtype, _device()
+    assert dtype in _TYPES, "expected a bf16 or fp32 tensor"
+    hq = _heads(q, q_out, wq, dtype, dev, tokens, d)
+    hk = None if k is None else ctypes.byref(_heads(k, k_out, wk, dtype, dev, tokens, d))
+    s = lib().csa2_norm_rope(None if rope is None else rope.ref, _TYPES[dtype], tokens, d,
+                             _ptr(pos, _I64, dev, (tokens,)), eps, ctypes.byref(hq), hk, _stream(stream, dev))
+    if s:
+        raise Csa2Error("csa2_norm_rope", s)
 
 
 def csa2_fp8_quantize(x, data, scale, stream=None):
     """x [rows, k] bf16 (dense rows) -> data [rows, k] E4M3 (or uint8), scale [ceil(k / 128), rows] fp32."""
     rows, k = x.shape
-    assert x.stride(1) == 1 or k == 1, "expected dense rows"
-    _check("csa2_fp8_quantize", lib().csa2_fp8_quantize(
-        rows, k, _ptr(x, _BF16, dense=False), x.stride(0), _ptr(data, _E4M3, x.shape),
-        _ptr(scale, _F32, (-(-k // 128), rows)), _stream(stream)))
+    xs, one = x.stride()
+    dev = _device()
+    assert one == 1 or k == 1, "expected dense rows"
+    s = lib().csa2_fp8_quantize(rows, k, _ptr(x, _BF16, dev, None, False), xs, _ptr(data, _E4M3, dev, (rows, k)),
+                                _ptr(scale, _F32, dev, (-(-k // 128), rows)), _stream(stream, dev))
+    if s:
+        raise Csa2Error("csa2_fp8_quantize", s)
 
 
 def csa2_fp8_quantize_weight(w, data, scale, stream=None):
     """w [n, k] bf16 -> data [n, k] E4M3 (or uint8), scale [ceil(n / 128), ceil(k / 128)] fp32."""
     n, k = w.shape
+    dev = _device()
     _check("csa2_fp8_quantize_weight", lib().csa2_fp8_quantize_weight(
-        n, k, _ptr(w, _BF16), _ptr(data, _E4M3, w.shape), _ptr(scale, _F32, (-(-n // 128), -(-k // 128))),
-        _stream(stream)))
+        n, k, _ptr(w, _BF16, dev), _ptr(data, _E4M3, dev, (n, k)),
+        _ptr(scale, _F32, dev, (-(-n // 128), -(-k // 128))), _stream(stream, dev)))
 
 
 def csa2_fp8_gemm(x, xs, w, ws, out, status=None, stream=None):
     """out [m, n] (bf16 or fp32, dense rows) = x [m, k] w [n, k]^T, E4M3 with the scales of csa2_fp8_quantize (xs)
     and csa2_fp8_quantize_weight (ws); status: a workspace for CSA2_DEV_TIMEOUT."""
     m, k = x.shape
-    n, nb = w.shape[0], -(-k // 128)
-    assert out.dtype in _TYPES, "expected a bf16 or fp32 tensor"
-    assert out.stride(1) == 1 or n == 1, "expected dense rows"
-    _check("csa2_fp8_gemm", lib().csa2_fp8_gemm(
-        m, n, k, _ptr(x, _E4M3), _ptr(xs, _F32, (nb, m)), _ptr(w, _E4M3, (n, k)), _ptr(ws, _F32, (-(-n // 128), nb)),
-        _TYPES[out.dtype], _ptr(out, (out.dtype,), (m, n), dense=False), max(out.stride(0), n), *_status(status),
-        _stream(stream)))
+    n, nb, dev, dtype = w.shape[0], -(-k // 128), _device(), out.dtype
+    o0, o1 = out.stride()
+    assert dtype in _TYPES, "expected a bf16 or fp32 tensor"
+    assert o1 == 1 or n == 1, "expected dense rows"
+    at, size = _status(status)
+    s = lib().csa2_fp8_gemm(m, n, k, _ptr(x, _E4M3, dev), _ptr(xs, _F32, dev, (nb, m)), _ptr(w, _E4M3, dev, (n, k)),
+                            _ptr(ws, _F32, dev, (-(-n // 128), nb)), _TYPES[dtype],
+                            _ptr(out, dtype, dev, (m, n), False), o0 if o0 > n else n, at, size, _stream(stream, dev))
+    if s:
+        raise Csa2Error("csa2_fp8_gemm", s)
 
 
 class PagedCache:
@@ -215,20 +258,32 @@ class PagedCache:
         self.table = page_table if page_table is not None else torch.full((batch, max_pages), -1, dtype=torch.int32,
                                                                           device=device)
         assert swa_slot is not None or n_slots >= batch, "expected a window ring per sequence"
+        dev = _device()
         self.c = csa2_paged_cache(
-            _ptr(self.l_data, _U8, (n_pages, page, 256)), _ptr(self.l_scale, _U8, (n_pages, page, 32)),
-            _ptr(self.k_data, _U8, (n_pages, page, 64)), _ptr(self.k_scale, _U8, (n_pages, page, 4)),
-            _ptr(self.swa, _U8, (n_slots, swa_cap, 512)), _ptr(self.table, _I32, (batch, max_pages)),
-            _ptr(swa_slot, _I32, (batch,)), n_pages, max_pages, n_slots, swa_cap, page)
+            _ptr(self.l_data, _U8, dev, (n_pages, page, 256)), _ptr(self.l_scale, _U8, dev, (n_pages, page, 32)),
+            _ptr(self.k_data, _U8, dev, (n_pages, page, 64)), _ptr(self.k_scale, _U8, dev, (n_pages, page, 4)),
+            _ptr(self.swa, _U8, dev, (n_slots, swa_cap, 512)), _ptr(self.table, _I32, dev, (batch, max_pages)),
+            _ptr(swa_slot, _I32, dev, (batch,)), n_pages, max_pages, n_slots, swa_cap, page)
+        self.dev = dev
         self.ref = ctypes.byref(self.c)
 
 
-def _append_row(x, weight, rope, batch, t, channels):
+    def on(self, batch):
+        """The current device, which has to be the cache's, for a call of `batch` sequences."""
+        dev = _device()
+        assert dev == self.dev, "expected the cache's device to be the current one"
+        assert batch <= self.batch, "expected at most the page table's sequences"
+        return dev
+
+
+def _append_row(x, weight, rope, dev, batch, t, channels):
     if x is None:
         return None
-    assert x.shape == (batch, t, channels) and x.stride(2) == 1, f"expected dense rows [{batch}, {t}, {channels}]"
-    return ctypes.byref(csa2_append_row(_ptr(x, _BF16, dense=False), x.stride(0), x.stride(1),
-                                        _ptr(weight, _BF16, (channels,)), rope.ref if rope is not None else None))
+    x0, x1, x2 = x.stride()
+    assert x2 == 1, f"expected dense rows [{batch}, {t}, {channels}]"
+    return ctypes.byref(csa2_append_row(_ptr(x, _BF16, dev, (batch, t, channels), False), x0, x1,
+                                        None if weight is None else _ptr(weight, _BF16, dev, (channels,)),
+                                        None if rope is None else rope.ref))
 
 
 def csa2_paged_append(cache: PagedCache, batch, t, pos, latent=None, idx_k=None, swa=None, rope=None, idx_rope=None,
@@ -238,41 +293,52 @@ def csa2_paged_append(cache: PagedCache, batch, t, pos, latent=None, idx_k=None,
     entries pos [B] int64, normed with the weights that are given and rotated (`rope` latent and window rows,
     unless swa_rope is given, `idx_rope` the key); length [B] int32: tokens of each sequence (None: t);
     rpos [B, t] int64: the tokens' positions for the rotation (None: those of the entries)."""
-    assert batch <= cache.batch, "expected at most the page table's sequences"
-    _check("csa2_paged_append", lib().csa2_paged_append(
-        cache.ref, batch, t, _ptr(pos, _I64, (batch,)), _ptr(length, _I32, (batch,)), _ptr(rpos, _I64, (batch, t)), eps,
-        _append_row(latent, w_latent, rope, batch, t, 512), _append_row(idx_k, w_idx_k, idx_rope, batch, t, 128),
-        _append_row(swa, w_swa, swa_rope if swa_rope is not None else rope, batch, t, 512), *_status(ws),
-        _stream(stream)))
+    dev = cache.on(batch)
+    at, size = _status(ws)
+    s = lib().csa2_paged_append(
+        cache.ref, batch, t, _ptr(pos, _I64, dev, (batch,)), _ptr(length, _I32, dev, (batch,)),
+        _ptr(rpos, _I64, dev, (batch, t)), eps, _append_row(latent, w_latent, rope, dev, batch, t, 512),
+        _append_row(idx_k, w_idx_k, idx_rope, dev, batch, t, 128),
+        _append_row(swa, w_swa, rope if swa_rope is None else swa_rope, dev, batch, t, 512), at, size,
+        _stream(stream, dev))
+    if s:
+        raise Csa2Error("csa2_paged_append", s)
 
 
 def csa2_paged_gather(cache: PagedCache, batch, idx, latent=None, key=None, ws=None, stream=None):
     """idx [B, n] int32 entries (-1: zeros) -> latent [B, n, 512] and key [B, n, 128] bf16 (either may be None)."""
-    assert batch <= cache.batch, "expected at most the page table's sequences"
-    n = idx.shape[1]
-    _check("csa2_paged_gather", lib().csa2_paged_gather(
-        cache.ref, batch, n, _ptr(idx, _I32, (batch, n)), _ptr(latent, _BF16, (batch, n, 512)),
-        _ptr(key, _BF16, (batch, n, 128)), *_status(ws), _stream(stream)))
+    dev, n = cache.on(batch), idx.shape[1]
+    at, size = _status(ws)
+    s = lib().csa2_paged_gather(cache.ref, batch, n, _ptr(idx, _I32, dev, (batch, n)),
+                                _ptr(latent, _BF16, dev, (batch, n, 512)), _ptr(key, _BF16, dev, (batch, n, 128)), at,
+                                size, _stream(stream, dev))
+    if s:
+        raise Csa2Error("csa2_paged_gather", s)
 
 
 def csa2_paged_attend(cache: PagedCache, batch, tq, qpos, q, idx, k, out, swa_begin=None, win=128, ratio=1,
                       sm_scale=0.0, out_f32=None, lse=None, ws=None, stream=None):
     """q [B*tq, 64, 512] bf16, idx [B*tq, k] int32 -> out [B*tq, 64, 512] bf16 (tensor cores)."""
-    assert batch <= cache.batch, "expected at most the page table's sequences"
-    rows = batch * tq
-    _check("csa2_paged_attend", lib().csa2_paged_attend(
-        cache.ref, batch, tq, _ptr(qpos, _I64, (rows,)), _ptr(q, _BF16, (rows, 64, 512)), _ptr(idx, _I32), k,
-        _ptr(swa_begin, _I64, (batch,)), win, ratio, sm_scale, _ptr(out, _BF16, (rows, 64, 512)),
-        _ptr(out_f32, _F32, (rows, 64, 512)), _ptr(lse, _F32, (rows, 64)), *_status(ws), _stream(stream)))
+    dev, rows = cache.on(batch), batch * tq
+    at, size = _status(ws)
+    s = lib().csa2_paged_attend(
+        cache.ref, batch, tq, _ptr(qpos, _I64, dev, (rows,)), _ptr(q, _BF16, dev, (rows, 64, 512)),
+        _ptr(idx, _I32, dev, (rows, k)), k, _ptr(swa_begin, _I64, dev, (batch,)), win, ratio, sm_scale,
+        _ptr(out, _BF16, dev, (rows, 64, 512)), _ptr(out_f32, _F32, dev, (rows, 64, 512)),
+        _ptr(lse, _F32, dev, (rows, 64)), at, size, _stream(stream, dev))
+    if s:
+        raise Csa2Error("csa2_paged_attend", s)
 
 
 def csa2_paged_index_topk(cache: PagedCache, batch, tq, qpos, idx_q, k, out_idx, ws, ratio=1, max_ctx=None, flags=0,
                           stream=None):
     """idx_q [B*tq, hi, 128] bf16 -> out_idx [B*tq, k] int32; ws: a LatentIndexWorkspace."""
-    assert batch <= cache.batch, "expected at most the page table's sequences"
-    rows = batch * tq
+    dev, rows, hi = cache.on(batch), batch * tq, idx_q.shape[-2]
     if max_ctx is None:
         max_ctx = cache.max_pages * cache.page
-    _check("csa2_paged_index_topk", lib().csa2_paged_index_topk(
-        cache.ref, batch, tq, _ptr(qpos, _I64, (rows,)), _ptr(idx_q, _BF16, (rows, idx_q.shape[-2], 128)),
-        idx_q.shape[-2], k, ratio, max_ctx, flags, _ptr(out_idx, _I32, (rows, k)), *_status(ws), _stream(stream)))
+    at, size = _status(ws)
+    s = lib().csa2_paged_index_topk(
+        cache.ref, batch, tq, _ptr(qpos, _I64, dev, (rows,)), _ptr(idx_q, _BF16, dev, (rows, hi, 128)), hi, k, ratio,
+        max_ctx, flags, _ptr(out_idx, _I32, dev, (rows, k)), at, size, _stream(stream, dev))
+    if s:
+        raise Csa2Error("csa2_paged_index_topk", s)
