@@ -111,6 +111,18 @@ __global__ void __launch_bounds__(256) fp8_weight_kernel(int64_t n, int k, const
     if (threadIdx.x == 0) scale[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
 
+// Waits for this thread's tensor-memory loads; v passes through, so that no use of it moves ahead.
+template <int N>
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&v)[N]) {
+    static_assert(N == 16 || N == 32, "registers of one load");
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < N; i += 16)
+        asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]),
+                          "+r"(v[i + 6]), "+r"(v[i + 7]), "+r"(v[i + 8]), "+r"(v[i + 9]), "+r"(v[i + 10]), "+r"(v[i + 11]),
+                          "+r"(v[i + 12]), "+r"(v[i + 13]), "+r"(v[i + 14]), "+r"(v[i + 15]));
+}
+
 // ---- the product ---------------------------------------------------------------------------------------
 
 constexpr uint64_t kWaitNs = 200000000ull;
@@ -272,7 +284,7 @@ __global__ void __launch_bounds__(192) fp8_cols_kernel(Fp8GemmArgs a, const __gr
                 uint32_t v[W];
                 const uint32_t at = tb + ((uint32_t)(32 * quad) << 16) + buf * NT + c;
                 if constexpr (W == 32) tmem_ld32(at, v); else tmem_ld16(at, v);
-                tmem_ld_wait();
+                tmem_ld_done(v);
 #pragma unroll
                 for (int j = 0; j < W; j += 4) {
                     const float4 s = *reinterpret_cast<const float4*>(sc + buf * NT + c + j);
@@ -316,6 +328,255 @@ __global__ void __launch_bounds__(192) fp8_cols_kernel(Fp8GemmArgs a, const __gr
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tb, G::kTmem);
+}
+
+// ---- large products: a pair of CTAs per tile ------------------------------------------------------------
+//
+// Tiles of 256 rows of x x 256 weight rows, one per cluster of two CTAs (cta_group::2: each CTA stages its
+// 128 rows of x and 128 of the weights, and holds its 128 rows' sums in tensor memory, so a stage's 32 KB
+// feed twice the products that one CTA's 48 KB would). Here a lane of tensor memory is a row of x: the
+// row's scale of a block is one number per thread. Persistent: each pair takes tiles in turn, rows
+// fastest, so that the pairs at work share weight rows in L2.
+// Warp 0 copies, warp 1 of the even CTA issues the MMAs for both, warps 4 .. 11 scale and add (two per
+// quarter of the lanes, 128 columns and 128 fp32 sums a thread). Two accumulators of 256 columns
+// alternate block by block: while the tensor cores write one, the other is read. Four of 128 columns, or
+// 16 reading warps, cost more in barriers than they hide (917 and 701 us where this takes 595, for
+// 4096 x 4096 x 32768).
+constexpr int kPairThreads = 384, kPairStages = 6, kPairStage = 2 * 128 * 128;
+constexpr int kPairSmem = kPairStages * kPairStage + (2 * kPairStages + 4) * 8 + 16 + 1024;
+// registers at launch: 168 x 384; the copying warpgroup gives up 112, the two others take 56 each
+constexpr uint32_t kPairRegsFew = 56, kPairRegsMany = 224;
+
+__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+// one arrival on the barrier at this address in both CTAs once every MMA issued before has completed
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+}
+__device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+// (no cluster-wide release: what it orders are tensor-memory reads, which the tcgen05 fences order; a
+// release over the cluster is a memory barrier, which the readers spent half their time in)
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// a box into this CTA's shared memory, counted on a barrier of the pair (an address in the cluster)
+__device__ __forceinline__ void tma_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// acc (two fp32) += v * s, element by element
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t s) {
+    asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(acc) : "r"(v0), "r"(v1), "l"(s));
+}
+
+// 32 of a row's sums to out[row][col ..]
+__device__ __forceinline__ void store32(const Fp8GemmArgs& a, int64_t row, int64_t col, const uint64_t* acc, bool wide) {
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        v[2 * i] = __uint_as_float((uint32_t)acc[i]);
+        v[2 * i + 1] = __uint_as_float((uint32_t)(acc[i] >> 32));
+    }
+    if (wide && col + 32 <= a.n) {
+        if (a.out_f32) {
+            float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + row * a.out_stride + col);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
+            uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + row * a.out_stride + col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+                    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                d[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (col + i < a.n) store_out(a, row, col + i, v[i]);
+    }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+fp8_pair_kernel(Fp8GemmArgs a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                int64_t mt, int64_t tiles) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + kPairStages * kPairStage);  // the even CTA's counts both CTAs' copies
+    uint64_t* empty = full + kPairStages;
+    uint64_t* tfull = empty + kPairStages;
+    uint64_t* tempty = tfull + 2;  // the even CTA's: both CTAs' warps
+    uint32_t* slot = reinterpret_cast<uint32_t*>(tempty + 2);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank();
+    const int64_t pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const int nb = (a.k + 127) / 128;
+
+    if (tid == 0) {
+        for (int i = 0; i < kPairStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 16);
+        }
+        mbar_fence_init();
+        prefetch_tmap(&wmap);
+        prefetch_tmap(&xmap);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers and tensor memory are there
+    tc_fence_after();
+    const uint32_t tb = *slot;
+    wait_prior_grid();
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !mbar_wait(bar, parity, kWaitNs)) {
+            ok = false;
+            set_status(a.status, CSA2_DEV_TIMEOUT);
+        }
+        return ok;
+    };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegsFew));
+        int st = 0;
+        uint32_t ph = 0;  // the stage in turn and how often (parity) the ring has gone round
+        auto next = [&]() {
+            if (++st == kPairStages) {
+                st = 0;
+                ph ^= 1u;
+            }
+        };
+        if (warp == 0 && lane == 0) {
+            for (int64_t t = pair; t < tiles && ok; t += pairs) {
+                const int m0 = (int)(t % mt * 256 + 128 * rank), n0 = (int)(t / mt * 256 + 128 * rank);
+                for (int b = 0; b < nb; ++b) {
+                    if (!wait(&empty[st], ph ^ 1u)) break;  // (passes at once in the first round)
+                    unsigned char* d = sm + st * kPairStage;
+                    if (rank == 0) mbar_expect_tx(&full[st], 2 * kPairStage);
+                    const uint32_t bar = at_rank(&full[st], 0);
+                    tma_2d_pair(d, &xmap, b * 128, m0, bar);
+                    tma_2d_pair(d + 128 * 128, &wmap, b * 128, n0, bar);
+                    next();
+                }
+            }
+            // every stage is read (its last commit has arrived) before this CTA may end
+            for (int j = 0; j < kPairStages; ++j) {
+                mbar_wait(&empty[st], ph ^ 1u, kWaitNs);
+                next();
+            }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            uint32_t i = 0;  // accumulators written so far
+            for (int64_t t = pair; t < tiles && ok; t += pairs) {
+                for (int b = 0; b < nb && ok; ++b) {
+                    if (!wait(&full[st], ph)) break;
+                    const uint32_t ad = smem_u32(sm + st * kPairStage), bd = ad + 128 * 128;
+                    const uint32_t buf = i & 1u;
+                    if (!wait(&tempty[buf], ((i >> 1) & 1u) ^ 1u)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        mma_f8_pair(tb + buf * 256, sw128_desc(ad + 32 * q), sw128_desc(bd + 32 * q), f8_idesc(256, 256), q > 0);
+                    commit_pair(&tfull[buf]);
+                    commit_pair(&empty[st]);
+                    ++i;
+                    next();
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairRegsMany));
+        const int quad = warp & 3, part = (warp - 4) >> 2;
+        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+        // 16-byte stores where every row starts on 16 bytes
+        const int per16 = a.out_f32 ? 4 : 8;
+        const bool wide = ((uintptr_t)a.out & 15) == 0 && a.out_stride % per16 == 0;
+        const uint32_t peer = at_rank(&tempty[0], 0);
+        uint32_t i = 0;
+        for (int64_t t = pair; t < tiles; t += pairs) {
+            const int64_t row = t % mt * 256 + 128 * rank + 32 * quad + lane;
+            const int64_t col = t / mt * 256 + 128 * part;
+            // the scales of the next two blocks are on their way (their product is formed when they are used,
+            // so that nothing waits for them before)
+            const bool live = row < a.m && col < a.n;
+            const float* xs = a.xs + (live ? row : 0);
+            const float* ws = a.ws + (live ? (col >> 7) * nb : 0);
+            const int64_t xstep = a.m;
+            uint64_t acc[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = 0ull;
+            float x0 = __ldg(xs), w0 = __ldg(ws), x1 = 0.f, w1 = 0.f;
+            if (nb > 1) {
+                x1 = __ldg(xs += xstep);
+                w1 = __ldg(ws + 1);
+            }
+            for (int b = 0; b < nb; ++b, ++i) {
+                float x2 = 0.f, w2 = 0.f;
+                if (b + 2 < nb) {
+                    x2 = __ldg(xs += xstep);
+                    w2 = __ldg(ws + b + 2);
+                }
+                const float f = x0 * w0;
+                const uint64_t s = ((uint64_t)__float_as_uint(f) << 32) | __float_as_uint(f);
+                x0 = x1, w0 = w1, x1 = x2, w1 = w2;
+                const uint32_t buf = i & 1u;
+                wait(&tfull[buf], (i >> 1) & 1u);
+                tc_fence_after();
+                const uint32_t at = tb + lanes + buf * 256 + 128 * part;
+                constexpr int W = 32;
+                uint32_t v[2][W];
+                tmem_ld32(at, v[0]);
+                tmem_ld_done(v[0]);
+#pragma unroll
+                for (int c = 0; c < 128 / W; ++c) {
+                    if (c + 1 < 128 / W) tmem_ld32(at + W * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+                    for (int j = 0; j < W / 2; ++j) fma2(acc[W / 2 * c + j], v[c & 1][2 * j], v[c & 1][2 * j + 1], s);
+                    if (c + 1 < 128 / W) tmem_ld_done(v[(c + 1) & 1]);
+                    if (c + 2 == 128 / W) {  // the last part is in registers: the accumulator may be written again
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (rank == 0) mbar_arrive(&tempty[buf]); else arrive_at(peer + 8 * buf);
+                        }
+                    }
+                }
+            }
+            if (row < a.m) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) store32(a, row, col + 32 * c, acc + 16 * c, wide);
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();  // no CTA ends while the other's MMAs or arrivals may reach it
+    tc_fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tb) : "memory");
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -378,6 +639,22 @@ cudaError_t launch_cols(const Fp8GemmArgs& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, k, a, wmap, xmap, split);
 }
 
+cudaError_t launch_pair(const Fp8GemmArgs& a, cudaStream_t s) {
+    CUtensorMap wmap, xmap;
+    cudaError_t e = make_map(&wmap, a.w, a.n, a.k, 128);
+    if (e == cudaSuccess) e = make_map(&xmap, a.x, a.m, a.k, 128);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+    int dev = 0, sms = 0;
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int64_t mt = (a.m + 255) / 256, tiles = mt * ((a.n + 255) / 256);
+    const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+    return launch_after_prior(fp8_pair_kernel, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), kPairSmem, s, a, wmap,
+                              xmap, mt, tiles);
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_rows(int64_t rows, int k, const uint16_t* x, int64_t x_stride, uint8_t* data, float* scale,
@@ -404,6 +681,8 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t s) {
     if (a.m <= 16) return launch_cols<16>(a, s);
     if (a.m <= 32) return launch_cols<32>(a, s);
     if (a.m <= 64) return launch_cols<64>(a, s);
+    const int64_t tiles = ((a.m + 255) / 256) * ((a.n + 255) / 256);
+    if (a.m > 128 && tiles >= 37) return launch_pair(a, s);
     return launch_cols<128>(a, s);
 }
 
