@@ -188,6 +188,26 @@ inline cudaError_t launch_after_prior(void (*kernel)(KArgs...), dim3 grid, dim3 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// the same in clusters of `size` CTAs along x
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, int size, size_t smem, cudaStream_t s,
+                                  Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)size;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- cp.async helpers ----------------------------------------------------------------------------
 __device__ __forceinline__ void cp_async16(void* smem, const void* gmem) {
     uint32_t s = (uint32_t)__cvta_generic_to_shared(smem);
@@ -526,6 +546,7 @@ __device__ __forceinline__ int64_t paged_slot(const PageMap& m, int b) {
 struct LatentAttendArgs {
     csa2_latent_cache c;
     PageMap pg;                // paged launches
+    int split;                 // paged launches: CTAs (a cluster) per row
     int rows, tq, k, win, ratio;
     const int64_t* qpos;       // [rows]
     const int64_t* swa_begin;  // [rows / tq] or NULL
@@ -539,7 +560,7 @@ struct LatentAttendArgs {
 };
 size_t latent_attend_smem_bytes();
 cudaError_t launch_latent_attend(const LatentAttendArgs& a, cudaStream_t s);
-cudaError_t launch_paged_attend(const LatentAttendArgs& a, cudaStream_t s);  // over the pages of a.pg
+cudaError_t launch_paged_attend(LatentAttendArgs a, cudaStream_t s);  // over the pages of a.pg
 
 constexpr int kLatMaxHI = 64;    // indexer query heads the latent indexer takes
 struct LatIndexArgs {

@@ -139,22 +139,6 @@ __host__ __device__ constexpr uint32_t f8_idesc(int m, int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// a float of CTA `rank`'s shared memory, at the address that `addr` has in this CTA's
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
-    float v;
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-                 : "=f"(v) : "r"(addr), "r"(rank) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ void store_out(const Fp8GemmArgs& a, int64_t i, int64_t j, float v) {
     if (a.out_f32)
         reinterpret_cast<float*>(a.out)[i * a.out_stride + j] = v;
@@ -623,20 +607,7 @@ cudaError_t launch_cols(const Fp8GemmArgs& a, cudaStream_t s) {
     int split = 1;
     while (split < 8 && tiles * split * 2 <= 160 && nb >= split * 4) split *= 2;
     if (tiles * split > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * split));
-    cfg.blockDim = dim3(G::kThreads);
-    cfg.dynamicSmemBytes = G::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)split;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k, a, wmap, xmap, split);
+    return launch_cluster(k, dim3((unsigned)(tiles * split)), dim3(G::kThreads), split, G::kSmem, s, a, wmap, xmap, split);
 }
 
 cudaError_t launch_pair(const Fp8GemmArgs& a, cudaStream_t s) {

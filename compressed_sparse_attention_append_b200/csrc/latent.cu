@@ -124,7 +124,11 @@ __device__ __forceinline__ float warp_sum16(float (&v)[16], int lane) {
 }
 
 // PAGED: the entries and window rings are those of a paged cache (a.pg); the row's indices are
-// translated to plane rows while they are staged, once per row.
+// translated to plane rows while they are staged, once per row. There a row's tiles may be split over the
+// a.split CTAs of a cluster (few rows leave most of the GPU idle): each runs its tiles as a row of its
+// own, and the partial results meet in shared memory: the CTAs' maxima and sums give each its factor
+// 2^(m_r - m) / l, each writes its scaled O over its L tile, and each adds up its share of the heads in
+// rank order.
 template <bool PAGED>
 __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -144,7 +148,9 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     const int key = tid & 127, qq = tid >> 7;      // load / dequantise: key, channels 128 qq ..
     const int half = qq >> 1;                      // channel half (blocks 4 half .. 4 half + 3)
     const int quad = warp & 3, cg = warp >> 2;     // softmax / epilogue: lanes 32 quad .., heads 16 cg ..
-    const int row = blockIdx.x, K = a.k;
+    const int split = PAGED ? a.split : 1;
+    const int rank = PAGED && split > 1 ? (int)cluster_rank() : 0;
+    const int row = PAGED ? (int)(blockIdx.x / (unsigned)split) : (int)blockIdx.x, K = a.k;
     wait_prior_grid();  // indices, cache and queries come from earlier work on the stream
 
     const int b = row / a.tq;
@@ -162,7 +168,9 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     if (PAGED && ring < 0 && a.win > 0 && threadIdx.x == 0) set_status(a.status, CSA2_DEV_BAD_PAGE);
     const int nwin = (row_ok && qpos >= lo && (!PAGED || ring >= 0)) ? (int)(qpos - lo + 1) : 0;
     const int ft = row_ok ? (K + kTile - 1) / kTile : 0;
-    const int nt = ft + (nwin > 0 ? 1 : 0);
+    const int all = ft + (nwin > 0 ? 1 : 0);                // the row's tiles; this CTA's: t0 .. t0 + nt - 1
+    const int t0 = PAGED ? all * rank / split : 0;
+    const int nt = PAGED ? all * (rank + 1) / split - t0 : all;
     const float scale2 = a.sm_scale * 1.4426950408889634f;  // logits in log2 units
     uint32_t* status = a.status;
 
@@ -185,7 +193,8 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
         for (int c = 0; c < 8; ++c) qv[c] = __ldg(src + c);
     }
     // the row's indices, checked once (an entry that is -1, not visible or out of range becomes -1)
-    for (int i = tid; i < (row_ok ? K : 0); i += kT) {
+    const int i0 = PAGED ? t0 * kTile : 0, i1 = PAGED && (t0 + nt) * kTile < K ? (t0 + nt) * kTile : K;
+    for (int i = i0 + tid; i < (row_ok ? i1 : 0); i += kT) {
         const int v = __ldg(a.idx + (size_t)row * K + i);
         const bool ok = v >= 0 && (int64_t)v <= qlast && (int64_t)v < a.c.cap;
         if (!ok && v != -1) set_status(status, CSA2_DEV_BAD_INDEX);
@@ -225,8 +234,8 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
         for (int i = 0; i < 4; ++i) raw[i] = make_uint4(0, 0, 0, 0);
         rsc = make_uint2(0, 0);
         kvalid = false;
-        if (j < ft) {
-            const int i = j * kTile + key;
+        if (j < nt && t0 + j < ft) {  // (the indices of this CTA's tiles are staged, no others)
+            const int i = (t0 + j) * kTile + key;
             const int v = i < K ? sidx[i] : -1;
             if (v >= 0) {
                 kvalid = true;
@@ -309,7 +318,7 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     // half 1), and the S^T k-steps of a half are issued as soon as the half is in shared memory, so
     // that dequantisation overlaps the tensor pipe. The softmax then runs on all 16 warps.
     for (int j = 0; j < nt; ++j) {
-        const bool fp4 = j < ft;  // CTA-uniform
+        const bool fp4 = t0 + j < ft;  // CTA-uniform
         const bool valid = kvalid;
         if (j > 0) wait_bar(half ? kBarO1 : kBarO0, (uint32_t)(j - 1) & 1u);
         dequant(fp4, valid);
@@ -434,6 +443,60 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
         if (lane < 16) red[quad * 64 + 16 * cg + lane] = r;
     }
     __syncthreads();
+    if (PAGED && split > 1) {
+        // this CTA's l and m per head, then the row's: its factor is 2^(m_r - m) / l (0 without a key)
+        if (tid < 64) s_l[tid] = nt > 0 ? (red[tid] + red[64 + tid]) + (red[128 + tid] + red[192 + tid]) : 0.f;
+        __syncthreads();
+        cluster_sync();
+        if (tid < 64) {
+            float m = -INFINITY, l = 0.f;
+            for (int r = 0; r < split; ++r) m = fmaxf(m, ld_cluster(smem_u32(&s_m[tid]), r));
+            for (int r = 0; r < split; ++r) {
+                const float mr = ld_cluster(smem_u32(&s_m[tid]), r), lr = ld_cluster(smem_u32(&s_l[tid]), r);
+                if (mr != -INFINITY) l = fmaf(lr, exp2f(mr - m), l);
+            }
+            const bool em = m == -INFINITY || !(l > 0.f);
+            s_al[tid] = em || s_m[tid] == -INFINITY ? 0.f : exp2f(s_m[tid] - m) / l;
+            if (a.lse && rank == 0) a.lse[(size_t)row * kLatHQ + tid] = em ? -INFINITY : m * 0.6931471805599453f + logf(l);
+        }
+        __syncthreads();
+        // every MMA that reads L has completed: O goes there as fp32 [head][512]
+        float* part = reinterpret_cast<float*>(Lt);
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            uint32_t v[16] = {};
+            if (nt > 0) {
+                tmem_ld16(tb + lane_base + kOCol + 64 * mt + 16 * cg, v);
+                tmem_ld_wait();
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float f = s_al[16 * cg + i];
+                part[(16 * cg + i) * kLatD + 128 * mt + 32 * quad + lane] = f != 0.f ? __uint_as_float(v[i]) * f : 0.f;
+            }
+        }
+        __syncthreads();
+        cluster_sync();
+        const int e0 = kLatHQ * rank / split * kLatD, e1 = kLatHQ * (rank + 1) / split * kLatD;
+        for (int e = e0 + 4 * tid; e < e1; e += 4 * kT) {
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int r = 0; r < split; ++r) {
+                const float4 x = ld_cluster4(smem_u32(part + e), r);
+                o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+            }
+            const size_t ob = (size_t)row * kLatHQ * kLatD + e;
+            const __nv_bfloat162 h0 = __floats2bfloat162_rn(o.x, o.y), h1 = __floats2bfloat162_rn(o.z, o.w);
+            *reinterpret_cast<uint2*>(a.out + ob) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+            if (a.out_f32) *reinterpret_cast<float4*>(a.out_f32 + ob) = o;
+        }
+        cluster_sync();  // the others have read this CTA's part
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == 0) tmem_dealloc(tb, kCols);
+        return;
+    }
     if (tid < 64) {
         const float l = (red[tid] + red[64 + tid]) + (red[128 + tid] + red[192 + tid]);
         s_l[tid] = l;
@@ -472,15 +535,34 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
 size_t latent_attend_smem_bytes() { return kSmem; }
 
 template <bool PAGED>
-static cudaError_t launch_rows(const LatentAttendArgs& a, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(latent_attend_kernel<PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmem);
+static cudaError_t launch_rows(const LatentAttendArgs& a, int split, cudaStream_t s) {
+    auto k = latent_attend_kernel<PAGED>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     if (a.rows == 0) return cudaSuccess;
-    return launch_after_prior(latent_attend_kernel<PAGED>, dim3((unsigned)a.rows), dim3(kT), kSmem, s, a);
+    if (split == 1) return launch_after_prior(k, dim3((unsigned)a.rows), dim3(kT), kSmem, s, a);
+    if (split > 8) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    return launch_cluster(k, dim3((unsigned)(a.rows * split)), dim3(kT), split, kSmem, s, a);
 }
 
-cudaError_t launch_latent_attend(const LatentAttendArgs& a, cudaStream_t s) { return launch_rows<false>(a, s); }
-cudaError_t launch_paged_attend(const LatentAttendArgs& a, cudaStream_t s) { return launch_rows<true>(a, s); }
+cudaError_t launch_latent_attend(const LatentAttendArgs& a, cudaStream_t s) { return launch_rows<false>(a, 1, s); }
+
+cudaError_t launch_paged_attend(LatentAttendArgs a, cudaStream_t s) {
+    // A tile takes about 4.6 us, what surrounds them 11 and the join 2: a row's tiles go over as many CTAs
+    // as leave every row's cluster on the GPU at once. How many of a size fit next to one another is a
+    // matter of the SMs per GPC (a second round of clusters costs more than the split gains).
+    constexpr struct { int size, rows; } kFit[] = {{16, 6}, {8, 14}, {6, 20}, {5, 24}, {4, 30}, {3, 42}, {2, 72}};
+    const int tiles = (a.k + kTile - 1) / kTile + (a.win > 0 ? 1 : 0);
+    a.split = 1;
+    for (const auto& f : kFit)
+        if (a.rows <= f.rows) {
+            a.split = f.size < tiles ? f.size : (tiles > 1 ? tiles : 1);
+            const int each = (tiles + a.split - 1) / a.split;
+            if (tiles > 0) a.split = (tiles + each - 1) / each;  // no smaller cluster has as few tiles per CTA
+            break;
+        }
+    return launch_rows<true>(a, a.split, s);
+}
 
 }  // namespace csa2
