@@ -16,7 +16,8 @@ struct RotateArgs {
     int d, rot, offset, layout, transposed;
     float mscale, eps, inv_d;
     int in_place;            // out is x and there is no norm: only the rotated channels are touched
-    int lanes, tb, hb, hblocks;  // lanes per row; tokens and heads per block; blocks per token group
+    int lanes, rounds;       // lanes per row; rows in turn per group of lanes, over those in flight
+    float inv_heads, inv_half;  // 1 / heads, 2 / rot
 };
 cudaError_t launch_rotate(const RotateArgs& a, int dtype, bool norm, cudaStream_t s);
 

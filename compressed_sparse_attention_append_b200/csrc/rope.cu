@@ -9,9 +9,10 @@
 // Both calls move each row once and compute little, so device memory bounds them. Split: a block
 // takes a few rows (a row: one head of one token), each row on 1 .. 32 lanes with 1 .. 8 vectors of
 // 16 (or 8) bytes per lane, all loads of the block's rows in flight before the sines and cosines
-// are formed; these are shared by the block's heads of a token through shared memory. A channel whose
-// partner sits in another vector (CSA2_ROPE_HALF) reads that vector too: it is in L1, since
-// the row's own lanes have just asked for it.
+// are formed; these are shared by the block's heads of a token through shared memory. The rows of a
+// block run on from one token to the next, so no head count leaves a block half empty. With
+// CSA2_ROPE_HALF a lane takes vectors in pairs, rot / 2 channels apart where they turn, so that both
+// channels of every rotated pair are its own.
 #include "csa2_internal.cuh"
 #include "csa2_layer.cuh"
 
@@ -63,116 +64,160 @@ __device__ __forceinline__ Vec<VB> pack(const float* f) {
     return v;
 }
 
-// One row per group of a.lanes lanes, CPL vectors per lane, ITER rows per group.
-template <typename T, int VB, int CPL, int ITER, bool NORM>
-__global__ void __launch_bounds__(kThr) rotate_kernel(RotateArgs a) {
+// One row per group of a.lanes lanes, CPL vectors per lane; ITER rows of a group are in flight, and with a
+// norm a group takes a.rounds * ITER rows in turn. Measured for 4096 tokens x 64 heads x 512, bf16: the
+// rotation alone is fastest with two rows in flight and one round (83 us, 6.4 TB/s); the norm, whose
+// instructions weigh as much as its bytes, with one row, eight rounds and five blocks an SM (99 us,
+// 5.5 TB/s; one round 108, two rows 118). Rows of 128 channels: 16384 tokens x 33 heads 81 us (3.4 TB/s), in
+// halves over the whole head 16384 x 20 heads 46 us (3.7 TB/s): shorter rows, more instructions per byte.
+template <typename T, int VB, int CPL, int ITER, bool NORM, bool HALF>
+__global__ void __launch_bounds__(kThr, NORM && CPL <= 2 ? (HALF ? 4 : 5) : 1) rotate_kernel(RotateArgs a) {
     constexpr int E = VB / (int)sizeof(T);
     using V = Vec<VB>;
-    extern __shared__ float2 cs[];  // [tokens of the block][rot / 2]
-    const int tid = threadIdx.x, lanes = a.lanes, per = kThr / lanes;
-    const int gl = tid & (lanes - 1), gr = tid / lanes;
-    const int64_t tok0 = (int64_t)(blockIdx.x / (unsigned)a.hblocks) * a.tb;
-    const int head0 = (int)(blockIdx.x % (unsigned)a.hblocks) * a.hb;
-    const int ntok = (int)(a.tokens - tok0 < a.tb ? a.tokens - tok0 : a.tb);
-    const int nh = a.heads - head0 < a.hb ? a.heads - head0 : a.hb;
-    const int nrows = ntok * nh, half = a.rot >> 1, nc = a.d / E;
-    wait_prior_grid();
-
-    V x[ITER][CPL], p[ITER][CPL];
-    int tl[ITER];
-    T* out[ITER];
-    const T* wt[ITER];
+    extern __shared__ float table[];  // [tokens of the block][rot / 2] cosines, then the sines
+    // where a row is always a warp's, its number, and all that follows from it, is the same in every lane
+    constexpr bool WARP = CPL > (HALF ? 2 : 1);
+    const int tid = threadIdx.x, lanes = WARP ? 32 : a.lanes, per = kThr / lanes;
+    const int gl = tid & (lanes - 1);
+    const int gr = WARP || lanes == 32 ? __shfl_sync(0xffffffffu, tid >> 5, 0) : tid / lanes;
+    const int rounds = NORM ? a.rounds : 1;
+    // the block's rows, in the order token, head: row0 .. row0 + nrows - 1, of tokens tok0 .. tok0 + ntok - 1
+    const int most = per * ITER * rounds;
+    const int64_t row0 = (int64_t)blockIdx.x * most, left = a.tokens * a.heads - row0;
+    const int nrows = left < most ? (int)left : most;
+    // (a 64-bit division costs as much as a row's arithmetic)
+    const int64_t tok0 = a.tokens * a.heads <= 0x7FFFFFFF ? (int64_t)((uint32_t)row0 / (uint32_t)a.heads) : row0 / a.heads;
+    const int head0 = (int)(row0 - tok0 * a.heads), ntok = (head0 + nrows - 1) / a.heads + 1;
+    const int half = a.rot >> 1;
+    // this lane's vectors: first element, whether it is there, whether it turns
+    int at[CPL];
+    bool there[CPL], turned[CPL];
 #pragma unroll
-    for (int it = 0; it < ITER; ++it) {
-        const int row = it * per + gr;
-        out[it] = nullptr;
-        tl[it] = 0;
-        wt[it] = nullptr;
-        if (row >= nrows) continue;
-        tl[it] = row / nh;
-        const int hh = head0 + row % nh;
-        const int64_t tok = tok0 + tl[it];
-        if (a.pos && a.pos[tok] < 0) continue;  // padding: nothing written
-        const bool isq = hh < a.q.heads;
-        const csa2_heads& H = isq ? a.q : a.k;
-        const int64_t h = isq ? hh : hh - a.q.heads;
-        const T* src = reinterpret_cast<const T*>(H.x) + tok * H.x_token + h * H.x_head;
-        out[it] = reinterpret_cast<T*>(H.out) + tok * H.out_token + h * H.out_head;
-        wt[it] = reinterpret_cast<const T*>(H.weight);
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-            const int ch = gl + c * lanes, r = ch * E - a.offset;  // first channel, within the rotated range
-            const bool turned = r >= 0 && r < a.rot;
-            if (ch < nc && (turned || !a.in_place)) x[it][c] = *reinterpret_cast<const V*>(src + ch * E);
-            if (ch < nc && turned && a.layout == CSA2_ROPE_HALF)
-                p[it][c] = *reinterpret_cast<const V*>(src + ch * E + (r < half ? half : -half));
+    for (int c = 0; c < CPL; ++c) {
+        if constexpr (HALF) {
+            // pairs of vectors: the rp pairs that turn, rp vectors apart, then the others (np pairs, np apart)
+            const int nc = a.d / E, rp = half / E, np = (nc - 2 * rp + 1) / 2, pi = gl + (c >> 1) * lanes, q = pi - rp;
+            const int o = q + (c & 1) * np, i = o < a.offset / E ? o : o + 2 * rp;
+            turned[c] = q < 0;
+            at[c] = turned[c] ? a.offset + (pi + (c & 1) * rp) * E : i * E;
+            there[c] = turned[c] || (q < np && o < nc - 2 * rp && !a.in_place);
+        } else {
+            at[c] = (gl + c * lanes) * E;
+            const int k = at[c] - a.offset;
+            turned[c] = at[c] < a.d && k >= 0 && k < a.rot;
+            there[c] = at[c] < a.d && (turned[c] || !a.in_place);
         }
     }
-    for (int i = tid; i < ntok * half; i += kThr)
-        cs[i] = turn(a.pos[tok0 + i / half], a.inv_freq[i % half], a.mscale, a.transposed);
-    __syncthreads();  // the table; also: every row of the block is loaded before one is stored (out == x)
+    wait_prior_grid();
 
+    V x[ITER][CPL];
+    int tl[ITER];
+    T* out[ITER];
+    bool isq[ITER];
+    float w[NORM ? CPL : 1][E];  // the weights of the rows so far (queries first)
+    bool have = false, have_q = false;
+    auto load = [&](int it, int row) {  // row `row` of the block into slot it
+        out[it] = nullptr;
+        if (row >= nrows) return;
+        tl[it] = (int)(((float)(head0 + row) + 0.5f) * a.inv_heads);  // the quotient by heads: below 2^17, exact
+        const int hh = head0 + row - tl[it] * a.heads;
+        const int64_t tok = tok0 + tl[it];
+        if (a.pos && a.pos[tok] < 0) return;  // padding: nothing written
+        isq[it] = hh < a.q.heads;
+        const csa2_heads& H = isq[it] ? a.q : a.k;
+        const int64_t h = isq[it] ? hh : hh - a.q.heads;
+        const T* src = reinterpret_cast<const T*>(H.x) + tok * H.x_token + h * H.x_head;
+        out[it] = reinterpret_cast<T*>(H.out) + tok * H.out_token + h * H.out_head;
 #pragma unroll
-    for (int it = 0; it < ITER; ++it) {
-        float r = 1.f;
-        if constexpr (NORM) {
-            float ss = 0.f;
+        for (int c = 0; c < CPL; ++c)
+            if (there[c]) x[it][c] = *reinterpret_cast<const V*>(src + at[c]);
+    };
 #pragma unroll
-            for (int c = 0; c < CPL; ++c) {
-                if (out[it] && gl + c * lanes < nc) {
-                    float f[E];
-                    unpack<T, VB>(x[it][c], f);
+    for (int it = 0; it < ITER; ++it) load(it, it * per + gr);
+    float* const sines = table + ntok * half;
+    for (int i = tid; i < ntok * half; i += kThr) {
+        const int t = (int)(((float)i + 0.5f) * a.inv_half);  // the quotient by half: below 2^14, exact
+        const float2 v = turn(a.pos[tok0 + t], a.inv_freq[i - t * half], a.mscale, a.transposed);
+        table[i] = v.x;
+        sines[i] = v.y;
+    }
+    __syncthreads();
+
+    for (int round = 0; round < rounds; ++round) {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) ss = fmaf(f[e], f[e], ss);
-                }
-            }
-            for (int o = lanes >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            r = rsqrtf(ss * a.inv_d + a.eps);
-        }
-        if (!out[it]) continue;
-        const float2* t = cs + tl[it] * half;
+        for (int it = 0; it < ITER; ++it) {
+            float r = 1.f;
+            if constexpr (NORM) {
+                float ss = 0.f;
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-            const int ch = gl + c * lanes, k = ch * E - a.offset;
-            const bool turned = k >= 0 && k < a.rot;
-            if (ch >= nc || (!turned && a.in_place)) continue;
-            float f[E];
-            unpack<T, VB>(x[it][c], f);
-            auto weigh = [&](float* v, int at) {
-                if constexpr (NORM) {
-                    if (wt[it]) {
-                        float w[E];
-                        unpack<T, VB>(*reinterpret_cast<const V*>(wt[it] + at), w);
+                for (int c = 0; c < CPL; ++c) {
+                    if (out[it] && there[c]) {
+                        float f[E];
+                        unpack<T, VB>(x[it][c], f);
 #pragma unroll
-                        for (int e = 0; e < E; ++e) v[e] *= r * w[e];
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < E; ++e) v[e] *= r;
+                        for (int e = 0; e < E; ++e) ss = fmaf(f[e], f[e], ss);
                     }
                 }
-            };
-            weigh(f, ch * E);
-            if (turned) {
-                if (a.layout == CSA2_ROPE_HALF) {
-                    float g[E];
-                    unpack<T, VB>(p[it][c], g);
-                    const bool first = k < half;
-                    weigh(g, ch * E + (first ? half : -half));
-                    const float2* u = t + (first ? k : k - half);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) f[e] = fmaf(f[e], u[e].x, first ? -g[e] * u[e].y : g[e] * u[e].y);
-                } else {
-                    const float2* u = t + (k >> 1);
+                for (int o = 16; o; o >>= 1)
+                    if (o < lanes) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                r = rsqrtf(ss * a.inv_d + a.eps);
+                if (out[it] && (!have || have_q != isq[it])) {  // (a block's rows are mostly of one kind)
+                    const T* wt = reinterpret_cast<const T*>(isq[it] ? a.q.weight : a.k.weight);
+                    have = true;
+                    have_q = isq[it];
 #pragma unroll
-                    for (int e = 0; e < E; e += 2) {
-                        const float2 v = u[e >> 1];
-                        const float y0 = fmaf(f[e], v.x, -f[e + 1] * v.y);
-                        f[e + 1] = fmaf(f[e + 1], v.x, f[e] * v.y);
-                        f[e] = y0;
+                    for (int c = 0; c < CPL; ++c) {
+                        if (wt && there[c])
+                            unpack<T, VB>(*reinterpret_cast<const V*>(wt + at[c]), w[c]);
+                        else
+#pragma unroll
+                            for (int e = 0; e < E; ++e) w[c][e] = 1.f;
                     }
                 }
             }
-            *reinterpret_cast<V*>(out[it] + ch * E) = pack<T, VB>(f);
+            if (out[it]) {
+                const float *cosines = table + tl[it] * half, *sn = sines + tl[it] * half;
+                constexpr int G = HALF ? 2 : 1;  // vectors that turn together
+#pragma unroll
+                for (int c = 0; c < CPL; c += G) {
+                    float f[G][E];
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        if (!there[c + g]) continue;
+                        unpack<T, VB>(x[it][c + g], f[g]);
+                        if constexpr (NORM) {
+#pragma unroll
+                            for (int e = 0; e < E; ++e) f[g][e] *= r * w[c + g][e];
+                        }
+                    }
+                    if (turned[c]) {
+                        if constexpr (HALF) {
+                            const int j = at[c] - a.offset;
+#pragma unroll
+                            for (int e = 0; e < E; ++e) {
+                                const float cv = cosines[j + e], sv = sn[j + e];
+                                const float y0 = fmaf(f[0][e], cv, -f[1][e] * sv);
+                                f[1][e] = fmaf(f[1][e], cv, f[0][e] * sv);
+                                f[0][e] = y0;
+                            }
+                        } else {
+                            const int j = (at[c] - a.offset) >> 1;
+#pragma unroll
+                            for (int e = 0; e < E; e += 2) {
+                                const float cv = cosines[j + e / 2], sv = sn[j + e / 2];
+                                const float y0 = fmaf(f[0][e], cv, -f[0][e + 1] * sv);
+                                f[0][e + 1] = fmaf(f[0][e + 1], cv, f[0][e] * sv);
+                                f[0][e] = y0;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+                        if (there[c + g]) *reinterpret_cast<V*>(out[it] + at[c + g]) = pack<T, VB>(f[g]);
+                }
+            }
+            if (round + 1 < rounds) load(it, ((round + 1) * ITER + it) * per + gr);
         }
     }
 }
@@ -229,36 +274,46 @@ int ceil_pow2(int x) {
     return p;
 }
 
-template <typename T, int VB, int CPL, int ITER, bool NORM>
+template <typename T, int VB, int CPL, int ITER, bool NORM, bool HALF>
 cudaError_t launch_vec(RotateArgs a, cudaStream_t s) {
-    const int rows = kThr / a.lanes * ITER;  // per block
-    if (a.heads >= rows) {
-        a.tb = 1;
-        a.hb = rows;
-    } else {
-        a.tb = rows / a.heads;
-        a.hb = a.heads;
-    }
-    a.hblocks = (a.heads + a.hb - 1) / a.hb;
-    const int64_t grid = (a.tokens + a.tb - 1) / a.tb * a.hblocks;
+    const int rows = kThr / a.lanes * ITER;  // per block and round
+    const int64_t all = a.tokens * a.heads;
+    // the table of a block of n rows: the tokens of n rows in a run
+    auto table = [&](int64_t n) {
+        const int64_t toks = (n - 1) / a.heads + 2;
+        return (size_t)(toks < n ? toks : n) * (a.rot / 2) * sizeof(float2);
+    };
+    // Rounds: the index arithmetic, the table and the weights are once per block, so with a norm a block takes
+    // up to eight rounds of rows while six blocks an SM remain and the table stays small. (One round's table
+    // is at most 33 KB: rows * rot / 2 <= 256 / lanes * ITER * lanes * CPL * E / 2 pairs with
+    // ITER * CPL * E <= 32, and one token more of up to 512 pairs.)
+    a.rounds = 1;
+    while (NORM && a.rounds < 8 && all >= (int64_t)148 * 6 * rows * a.rounds * 2 && table((int64_t)rows * a.rounds * 2) <= 16384)
+        a.rounds *= 2;
+    const int64_t most = (int64_t)rows * a.rounds, grid = (all + most - 1) / most;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    // at most 32 KB: tb * rot / 2 <= rows * d / 2 <= 256 / lanes * ITER * lanes * CPL * E / 2 pairs,
-    // ITER * CPL * E <= 32
-    const size_t smem = (size_t)a.tb * (a.rot / 2) * sizeof(float2);
-    return launch_after_prior(rotate_kernel<T, VB, CPL, ITER, NORM>, dim3((unsigned)grid), dim3(kThr), smem, s, a);
+    a.inv_heads = 1.f / (float)a.heads;
+    a.inv_half = a.rot ? 2.f / (float)a.rot : 0.f;
+    const size_t smem = table(most);
+    return launch_after_prior(rotate_kernel<T, VB, CPL, ITER, NORM, HALF>, dim3((unsigned)grid), dim3(kThr), smem, s, a);
 }
 
-template <typename T, int VB, bool NORM>
+template <typename T, int VB, bool NORM, bool HALF>
 cudaError_t launch_rows(RotateArgs a, cudaStream_t s) {
-    const int nc = a.d / (VB / (int)sizeof(T));
-    a.lanes = nc < 32 ? ceil_pow2(nc) : 32;
+    constexpr int G = HALF ? 2 : 1;  // vectors that a lane takes together
+    const int nc = a.d / (VB / (int)sizeof(T)), need = (nc + G - 1) / G;
+    a.lanes = need < 32 ? ceil_pow2(need) : 32;
     // several rows per group where the blocks still fill the GPU (about eight of 256 threads an SM);
     // below that a block does less, for latency
     const bool many = a.tokens * a.heads >= (int64_t)148 * 8 * (kThr / a.lanes) * 2;
-    if (nc <= 32) return many ? launch_vec<T, VB, 1, 4, NORM>(a, s) : launch_vec<T, VB, 1, 1, NORM>(a, s);
-    if (nc <= 64) return many ? launch_vec<T, VB, 2, 2, NORM>(a, s) : launch_vec<T, VB, 2, 1, NORM>(a, s);
-    if (nc <= 128) return launch_vec<T, VB, 4, 1, NORM>(a, s);
-    return launch_vec<T, VB, 8, 1, NORM>(a, s);
+    if (need <= 32)
+        return many ? launch_vec<T, VB, G, NORM ? 1 : 4 / G, NORM, HALF>(a, s) : launch_vec<T, VB, G, 1, NORM, HALF>(a, s);
+    if (need <= 64)
+        return many ? launch_vec<T, VB, 2 * G, NORM || HALF ? 1 : 2, NORM, HALF>(a, s)
+                    : launch_vec<T, VB, 2 * G, 1, NORM, HALF>(a, s);
+    if (need <= 128) return launch_vec<T, VB, 4 * G, 1, NORM, HALF>(a, s);
+    if constexpr (!HALF) return launch_vec<T, VB, 8, 1, NORM, HALF>(a, s);  // (256 vectors at most)
+    return cudaErrorInvalidValue;
 }
 
 template <typename T, bool NORM>
@@ -277,8 +332,9 @@ cudaError_t launch_typed(const RotateArgs& a, cudaStream_t s) {
         }
         return true;
     };
-    if (fits(16)) return launch_rows<T, 16, NORM>(a, s);
-    if (fits(8)) return launch_rows<T, 8, NORM>(a, s);
+    const bool half = a.layout == CSA2_ROPE_HALF;
+    if (fits(16)) return half ? launch_rows<T, 16, NORM, true>(a, s) : launch_rows<T, 16, NORM, false>(a, s);
+    if (fits(8)) return half ? launch_rows<T, 8, NORM, true>(a, s) : launch_rows<T, 8, NORM, false>(a, s);
     const int64_t grid = (a.tokens * a.heads + kThr / 32 - 1) / (kThr / 32);
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     return launch_after_prior(rotate_scalar_kernel<T, NORM>, dim3((unsigned)grid), dim3(kThr), 0, s, a);
