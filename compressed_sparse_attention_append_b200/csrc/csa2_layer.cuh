@@ -39,6 +39,8 @@ struct PagedAppendArgs {
     const int64_t* rpos;
     double eps;
     AppendRow row[3];        // latent, indexer key, window
+    int kinds, kind[3];      // those that are appended
+    int most_rot;            // channels of the widest rotation
     uint32_t* status;
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);

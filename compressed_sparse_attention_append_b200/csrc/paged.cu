@@ -4,12 +4,21 @@
 // [C] "DeepSeek-V4.1-Flash: Pushing KV Cache Compression to 890 Bytes per Token", sec. XI: cached
 // values are quantised after the rotation. Here one kernel does
 //   y = R_pos(x * w / sqrt(mean(x^2) + eps)),  then the codecs of csa2.h on y,
-// with nothing rounded in between, and every code and scale is the one that y has: a value next to a
-// rounding border of a 4-bit code falls on the wrong side in fp32, so norm, rotation and quotients
-// are formed in 64 bits and reach the conversion instructions by rounding to odd.
+// with nothing rounded in between, and every code and scale is the one that y has. A value next to a
+// rounding border of a 4-bit code falls on the wrong side in fp32, so:
+//   - y is formed in fp32 with a bound e on its error, and both y - e and y + e are converted: where the two
+//     conversions agree (codes and scales are monotone in y) the code is y's;
+//   - a row in which any two differ (one in several hundred) is formed again in 64 bits, norm, rotation
+//     and quotients, and reaches the conversion instructions by rounding to odd. Rows without a norm,
+//     whose bf16 values lie on borders often, are always formed so.
+// The error of fp32: the sum of squares is off by 4 roundings (a lane's 16 as a tree, the lanes' sums in 64 bits),
+// its root by half of that and 2^-23.4, the product by 2^-24, the quotient by 2^-23 more: below 2^-21.3. Cosine
+// and sine are off by 2^-21.4. So e = 2^-21 |y|, and 2^-20 m (|a| + |b|) for the channels of a rotated pair
+// (a, b), cover y and its quotient.
 //
 // Work split: one warp per row (a token's latent, indexer key or window row), 16 channels per lane
-// (one scale block of the latent) or 4 (an eighth of an MXFP4 block).
+// (one scale block of the latent) or 4 (an eighth of an MXFP4 block). A row's rotated pairs are turned
+// by as many lanes, one pair each, through shared memory.
 #include "csa2_internal.cuh"
 #include "csa2_layer.cuh"
 
@@ -17,7 +26,8 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kWarps = 4;  // per block
+constexpr int kWarps = 4;    // per block
+constexpr int kBlocks = 12;  // per SM (registers): a row is a chain of loads, so many rows at once
 constexpr double kInvPi = 0.31830988618379067154;
 
 // Rounding to odd: the fp32 value next to v towards zero, its last bit set unless it is v. A further
@@ -27,17 +37,21 @@ __device__ __forceinline__ float to_odd(double v) {
     return (double)f == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
+// A warp's shared memory: 16 bytes per rotated channel of the widest rotation (channel k of the rotated range).
 struct WarpMem {
-    double2 cs[256];   // cos, sin of the row's pairs
-    float xw[kLatD];   // x * w, exact in fp32 (two bf16 factors)
+    unsigned char* p;
+    int rot;
+    __device__ __forceinline__ float* y() const { return reinterpret_cast<float*>(p); }             // values
+    __device__ __forceinline__ float* err() const { return reinterpret_cast<float*>(p) + rot; }     // and their errors
+    __device__ __forceinline__ double& xw(int k) const { return reinterpret_cast<double*>(p)[k]; }  // 64-bit rows: x * w
+    __device__ __forceinline__ double2& cs(int j) const {                                           // and cos, sin of pair j
+        return reinterpret_cast<double2*>(p + 8 * (size_t)rot)[j];
+    }
 };
 
-// N channels of this lane, normed and rotated (64 bits); CH = 32 N channels in the row.
+// this lane's N channels of a row of 32 N
 template <int N>
-__device__ __forceinline__ void normed_row(const AppendRow& R, const uint16_t* src, int64_t rpos, double eps,
-                                           WarpMem& sm, int lane, double (&y)[N]) {
-    constexpr int CH = 32 * N;
-    float x[N];
+__device__ __forceinline__ void load_row(const uint16_t* src, int lane, float (&x)[N]) {
     if constexpr (N == 16) {
         load16_bf16(src + lane * 16, x);
     } else {
@@ -47,58 +61,300 @@ __device__ __forceinline__ void normed_row(const AppendRow& R, const uint16_t* s
         x[2] = __uint_as_float(v.y << 16);
         x[3] = __uint_as_float(v.y & 0xFFFF0000u);
     }
+}
+// half turns of pos * f, in [-1, 1]
+__device__ __forceinline__ double half_turns(int64_t pos, double f) {
+    const double h = ((double)pos * f) * kInvPi;
+    return h - 2.0 * rint(0.5 * h);
+}
+// the channels of pair j within the rotated range
+__device__ __forceinline__ int2 pair_of(const AppendRow& R, int j) {
+    const bool inter = R.layout == CSA2_ROPE_INTERLEAVED;
+    return make_int2(inter ? 2 * j : j, inter ? 2 * j + 1 : j + (R.rot >> 1));
+}
+
+// ---- rows in 64 bits -----------------------------------------------------------------------------------
+
+// N channels of this lane, normed and rotated; CH = 32 N channels in the row.
+template <int N>
+__device__ __forceinline__ void exact_row(const AppendRow& R, const uint16_t* src, int64_t rpos, double eps,
+                                          const WarpMem& sm, int lane, double (&y)[N]) {
+    constexpr int CH = 32 * N;
+    float x[N];
+    load_row<N>(src, lane, x);
     double r = 1.0;
     if (R.weight) {
         double ss = 0.0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) ss += (double)(x[i] * x[i]);  // (exact products)
+        for (int i = 0; i < N; ++i) ss = fma((double)x[i], (double)x[i], ss);
         for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         r = 1.0 / sqrt(ss / CH + eps);
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] *= bf16_bits_to_f32(R.weight[lane * N + i]);
     }
-    __syncwarp();  // the row before is done with the shared memory
-    if (R.inv_freq) {
-        const int half = R.rot >> 1;
 #pragma unroll
-        for (int i = 0; i < N; ++i) sm.xw[lane * N + i] = x[i];
-        for (int j = lane; j < half; j += 32) {
-            double h = ((double)rpos * R.inv_freq[j]) * kInvPi, s, c;
-            h -= 2.0 * rint(0.5 * h);
-            sincospi(h, &s, &c);
-            sm.cs[j] = make_double2(c * R.mscale, s * R.mscale);
+    for (int i = 0; i < N; ++i)  // (exact: two bf16 factors)
+        y[i] = R.weight ? (double)x[i] * (double)bf16_bits_to_f32(R.weight[lane * N + i]) : (double)x[i];
+    __syncwarp();
+    if (R.inv_freq) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int k = lane * N + i - R.offset;
+            if (k >= 0 && k < R.rot) sm.xw(k) = y[i];
+        }
+        for (int j = lane; j < (R.rot >> 1); j += 32) {
+            double s, c;
+            sincospi(half_turns(rpos, R.inv_freq[j]), &s, &c);
+            sm.cs(j) = make_double2(c * R.mscale, s * R.mscale);
         }
         __syncwarp();
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int ch = lane * N + i, k = ch - R.offset;
-        y[i] = (double)x[i] * r;
+        const int k = lane * N + i - R.offset;
+        y[i] *= r;
         if (R.inv_freq && k >= 0 && k < R.rot) {
-            const int half = R.rot >> 1;
-            const bool inter = R.layout == CSA2_ROPE_INTERLEAVED;
-            const int j = inter ? k >> 1 : (k < half ? k : k - half);
-            const bool first = inter ? !(k & 1) : k < half;
-            const int other = inter ? (first ? ch + 1 : ch - 1) : (first ? ch + half : ch - half);
-            const double2 t = sm.cs[j];
-            const double z = (double)sm.xw[other] * r;
-            y[i] = y[i] * t.x + (first ? -z * t.y : z * t.y);
+            const int j = R.layout == CSA2_ROPE_INTERLEAVED ? k >> 1 : (k < (R.rot >> 1) ? k : k - (R.rot >> 1));
+            const int2 p = pair_of(R, j);
+            const double2 t = sm.cs(j);
+            const double z = sm.xw(k == p.x ? p.y : p.x) * r;
+            y[i] = y[i] * t.x + (k == p.x ? -z * t.y : z * t.y);
         }
     }
 }
 
-__global__ void __launch_bounds__(32 * kWarps) paged_append_kernel(PagedAppendArgs a) {
-    __shared__ WarpMem mem[kWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    WarpMem& sm = mem[warp];
-    const int64_t id = (int64_t)blockIdx.x * kWarps + warp;
+// eight fp32 -> eight E2M1 codes, RNE, saturating
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// a row's 16-channel E2M1 block, 4 MXFP4 channels or 16 window channels of this lane
+struct Coded {
+    uint4 codes;
+    uint32_t scale;
+};
+
+__device__ __noinline__ Coded exact_latent(const AppendRow& R, const uint16_t* src, int64_t rpos, double eps, const WarpMem& sm,
+                                           int lane) {
+    double y[16], top = 0.0;
+    exact_row<16>(R, src, rpos, eps, sm, lane, y);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = fmax(top, fabs(y[j]));
+    Coded c{};
+    c.scale = f32x2_to_e4m3x2(to_odd(top / 6.0), 0.f) & 0xFFu;
+    const float s = e4m3_to_f32((uint8_t)c.scale);
+    if (s != 0.f) {
+        const double inv = 1.0 / (double)s;
+        uint32_t w[2] = {0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            w[j >> 2] |= f32x2_to_e2m1x2(to_odd(y[2 * j] * inv), to_odd(y[2 * j + 1] * inv)) << (8 * (j & 3));
+        c.codes.x = w[0];
+        c.codes.y = w[1];
+    }
+    return c;
+}
+
+__device__ __noinline__ Coded exact_key(const AppendRow& R, const uint16_t* src, int64_t rpos, double eps, const WarpMem& sm,
+                                        int lane) {
+    double y[4];
+    exact_row<4>(R, src, rpos, eps, sm, lane, y);
+    double top = fmax(fmax(fabs(y[0]), fabs(y[1])), fmax(fabs(y[2]), fabs(y[3])));
+    for (int o = 4; o; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));  // the block's 8 lanes
+    Coded c{};
+    if (top > 0.0) {
+        const int sb = ilogb(top) - 2 + 127;
+        c.scale = (uint32_t)(sb < 0 ? 0 : (sb > 254 ? 254 : sb));
+        const double inv = ldexp(1.0, 127 - (int)c.scale);
+        c.codes.x = f32x2_to_e2m1x2(to_odd(y[0] * inv), to_odd(y[1] * inv)) |
+                    (f32x2_to_e2m1x2(to_odd(y[2] * inv), to_odd(y[3] * inv)) << 8);
+    }
+    return c;
+}
+
+__device__ __noinline__ Coded exact_window(const AppendRow& R, const uint16_t* src, int64_t rpos, double eps, const WarpMem& sm,
+                                           int lane) {
+    double y[16];
+    exact_row<16>(R, src, rpos, eps, sm, lane, y);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        w[j] = f32x2_to_e4m3x2(to_odd(y[4 * j]), to_odd(y[4 * j + 1])) |
+               (f32x2_to_e4m3x2(to_odd(y[4 * j + 2]), to_odd(y[4 * j + 3])) << 16);
+    return Coded{make_uint4(w[0], w[1], w[2], w[3]), 0u};
+}
+
+// ---- rows in 32 bits, with the bound of each value's error --------------------------------------------------
+
+constexpr float kErr = 1.f / 2097152.f, kErrTurn = 1.f / 1048576.f;  // 2^-21, 2^-20
+
+// y, and L: a value y[i] is within |y[i]| kErr + L of the row's (L: the largest bound of this lane's rotated
+// channels). False where fp32 cannot hold the row's norm (squares past its range): no bound is valid then.
+template <int N>
+__device__ __forceinline__ bool quick_row(const AppendRow& R, const uint16_t* src, int64_t rpos, float eps,
+                                          const WarpMem& sm, int lane, float (&y)[N], float& L) {
+    float w[N];
+    load_row<N>(src, lane, y);
+    load_row<N>(R.weight, lane, w);
+    // sine and cosine of this lane's first pair are formed while the row is on its way
+    const int half = R.inv_freq ? R.rot >> 1 : 0;
+    float c0 = 0.f, s0 = 0.f;
+    if (lane < half) sincospif((float)half_turns(rpos, R.inv_freq[lane]), &s0, &c0);
+    // the lane's squares (exact) as a tree, the lanes' sums in 64 bits
+    float t[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) t[i] = fmaf(y[2 * i + 1], y[2 * i + 1], y[2 * i] * y[2 * i]);
+#pragma unroll
+    for (int o = N / 4; o; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) t[i] += t[i + o];
+    double ss = (double)t[0];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    // 1 / sqrt with one step of Newton's iteration, the product's rounding carried along
+    const float mean = (float)fma(ss, 1.0 / (32 * N), (double)eps), r0 = rsqrtf(mean), h = mean * r0;
+    const float r = fmaf(0.5f * r0, fmaf(-h, r0, 1.f) - fmaf(mean, r0, -h) * r0, r0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = (y[i] * w[i]) * r;  // (two bf16 factors: exact)
+    L = 0.f;
+    if (half) {
+        const int k0 = lane * N - R.offset;  // this lane's first channel within the rotated range
+        const bool mine = k0 < R.rot && k0 + N > 0;
+        // all of its channels turn, at a place that allows vectors
+        const bool whole = k0 >= 0 && k0 + N <= R.rot && !((k0 | R.rot) & 3);
+        float *const ys = sm.y(), *const es = sm.err();
+        __syncwarp();  // the row before is done with the shared memory
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4)
+                *reinterpret_cast<float4*>(ys + k0 + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+        } else if (mine) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (k0 + i >= 0 && k0 + i < R.rot) ys[k0 + i] = y[i];
+        }
+        __syncwarp();
+        const float m = (float)R.mscale, me = fabsf(m) * kErrTurn;
+        for (int j = lane; j < half; j += 32) {
+            if (j != lane) sincospif((float)half_turns(rpos, R.inv_freq[j]), &s0, &c0);
+            const int2 p = pair_of(R, j);
+            const float a = ys[p.x], b = ys[p.y], err = (fabsf(a) + fabsf(b)) * me;
+            ys[p.x] = m * fmaf(a, c0, -b * s0);
+            ys[p.y] = m * fmaf(b, c0, a * s0);
+            es[p.x] = es[p.y] = err;
+        }
+        __syncwarp();
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(ys + k0 + i), e = *reinterpret_cast<const float4*>(es + k0 + i);
+                y[i] = v.x, y[i + 1] = v.y, y[i + 2] = v.z, y[i + 3] = v.w;
+                L = fmaxf(L, fmaxf(fmaxf(e.x, e.y), fmaxf(e.z, e.w)));
+            }
+        } else if (mine) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (k0 + i >= 0 && k0 + i < R.rot) {
+                    y[i] = ys[k0 + i];
+                    L = fmaxf(L, es[k0 + i]);
+                }
+            }
+        }
+    }
+    return mean >= 1e-25f && mean <= 1e34f;
+}
+
+// Each returns whether every code (and scale) of the warp's row is certain.
+__device__ __forceinline__ bool quick_latent(const float (&y)[16], float L, Coded& c) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(y[i]));
+    const float err = fmaf(top, kErr, L);
+    const uint32_t sc = f32x2_to_e4m3x2((top - err) * (1.f / 6.f), (top + err) * (1.f / 6.f));
+    c.scale = sc & 0xFFu;
+    const float s = e4m3_to_f32((uint8_t)c.scale), inv = s != 0.f ? 1.f / s : 0.f, d = L * inv;
+    uint32_t lo[2], hi[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float l[8], u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float a = y[8 * h + j] * inv, da = fmaf(fabsf(a), kErr, d);
+            l[j] = a - da;
+            u[j] = a + da;
+        }
+        lo[h] = e2m1x8(l);
+        hi[h] = e2m1x8(u);
+    }
+    const bool none = s == 0.f;  // a scale of 0: codes +0
+    c.codes.x = none ? 0u : lo[0];
+    c.codes.y = none ? 0u : lo[1];
+    return __all_sync(0xffffffffu, c.scale == (sc >> 8) && (none || (lo[0] == hi[0] && lo[1] == hi[1])));
+}
+
+__device__ __forceinline__ bool quick_key(const float (&y)[4], float L, Coded& c) {
+    float top = 0.f, most = L;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(y[i]));
+#pragma unroll
+    for (int o = 4; o; o >>= 1) {  // the block's 8 lanes
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    const float err = fmaf(top, kErr, most), hi = top + err;
+    // the exponents of both ends: all zeros, or far above the smallest normal number (w / sqrt(mean) is then
+    // normal wherever it matters)
+    const int xl = (int)(__float_as_uint(fmaxf(top - err, 0.f)) >> 23), xh = (int)(__float_as_uint(hi) >> 23);
+    const bool sure = hi == 0.f || (xl == xh && xl > 64 && xl < 255);
+    c.scale = hi == 0.f ? 0u : (uint32_t)(xl - 2);
+    const float inv = hi == 0.f ? 0.f : __uint_as_float((uint32_t)(254 - (xl - 2)) << 23);  // 2^(127 - scale)
+    const float d = L * inv;
+    uint32_t l = 0u, h = 0u;
+    if (hi != 0.f) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float a = y[2 * j] * inv, b = y[2 * j + 1] * inv;
+            const float da = fmaf(fabsf(a), kErr, d), db = fmaf(fabsf(b), kErr, d);
+            l |= f32x2_to_e2m1x2(a - da, b - db) << (8 * j);
+            h |= f32x2_to_e2m1x2(a + da, b + db) << (8 * j);
+        }
+    }
+    c.codes.x = l;
+    return __all_sync(0xffffffffu, sure && l == h);
+}
+
+__device__ __forceinline__ bool quick_window(const float (&y)[16], float L, Coded& c) {
+    uint32_t lo[4] = {}, hi[4] = {};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float a = y[2 * j], b = y[2 * j + 1], da = fmaf(fabsf(a), kErr, L), db = fmaf(fabsf(b), kErr, L);
+        lo[j >> 1] |= f32x2_to_e4m3x2(a - da, b - db) << (16 * (j & 1));
+        hi[j >> 1] |= f32x2_to_e4m3x2(a + da, b + db) << (16 * (j & 1));
+    }
+    c.codes = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    return __all_sync(0xffffffffu, lo[0] == hi[0] && lo[1] == hi[1] && lo[2] == hi[2] && lo[3] == hi[3]);
+}
+
+// (the arguments stay in constant memory: the 64-bit functions take references into them)
+__global__ void __launch_bounds__(32 * kWarps, kBlocks) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const WarpMem sm{smem + 16 * (size_t)a.most_rot * warp, a.most_rot};
     wait_prior_grid();  // the rows come from, and the slots may still be read by, earlier work
-    if (id >= (int64_t)a.batch * a.t * 3) return;
-    const int kind = (int)(id % 3);
-    const int64_t tok = id / 3;
-    const int b = (int)(tok / a.t), i = (int)(tok % a.t);
+    const int64_t tok = (int64_t)blockIdx.x * kWarps + warp, tokens = (int64_t)a.batch * a.t;
+    if (tok >= tokens) return;
+    const int kind = a.kind[blockIdx.y];
+    // (in 32 bits where they suffice: a 64-bit division costs a fifth of a row's arithmetic)
+    const int b = tokens <= 0x7FFFFFFF ? (int)((uint32_t)tok / (uint32_t)a.t) : (int)(tok / a.t);
+    const int i = (int)(tok - (int64_t)b * a.t);
     const AppendRow& R = a.row[kind];
-    if (!R.x) return;
     const int64_t p0 = a.pos[b], p = p0 + i;
     const int n = a.len ? a.len[b] : a.t;
     const bool tell = i == 0 && lane == 0;
@@ -110,6 +366,8 @@ __global__ void __launch_bounds__(32 * kWarps) paged_append_kernel(PagedAppendAr
     if (i >= n) return;  // padding
     const uint16_t* src = R.x + (int64_t)b * R.x_batch + (int64_t)i * R.x_token;
     const int64_t rpos = a.rpos ? a.rpos[tok] : p;
+    const float eps = (float)a.eps;
+    Coded c{};
     if (kind == 2) {
         // the ring keeps the latest swa_cap tokens: an older one of this call shares its slot with a newer one
         if ((int64_t)i < (int64_t)n - a.c.swa_cap) return;
@@ -118,15 +376,14 @@ __global__ void __launch_bounds__(32 * kWarps) paged_append_kernel(PagedAppendAr
             if (lane == 0) set_status(a.status, CSA2_DEV_BAD_PAGE);
             return;
         }
-        double y[16];
-        normed_row<16>(R, src, rpos, a.eps, sm, lane, y);
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = f32x2_to_e4m3x2(to_odd(y[4 * j]), to_odd(y[4 * j + 1])) |
-                   (f32x2_to_e4m3x2(to_odd(y[4 * j + 2]), to_odd(y[4 * j + 3])) << 16);
+        bool sure = false;
+        if (R.weight) {
+            float y[16], L;
+            sure = quick_row<16>(R, src, rpos, eps, sm, lane, y, L) && quick_window(y, L, c);
+        }
+        if (!sure) c = exact_window(R, src, rpos, a.eps, sm, lane);
         uint8_t* dst = a.c.swa + (slot * a.c.swa_cap + (p & (a.c.swa_cap - 1))) * kLatSwa + lane * 16;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(dst) = c.codes;
         return;
     }
     const int64_t row = paged_row(a.pg, b, p);
@@ -134,39 +391,23 @@ __global__ void __launch_bounds__(32 * kWarps) paged_append_kernel(PagedAppendAr
         if (lane == 0) set_status(a.status, CSA2_DEV_BAD_PAGE);
         return;
     }
+    bool sure = false;
     if (kind == 0) {
-        double y[16];
-        normed_row<16>(R, src, rpos, a.eps, sm, lane, y);
-        double top = 0.0;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) top = fmax(top, fabs(y[j]));
-        const uint8_t sc = (uint8_t)f32x2_to_e4m3x2(to_odd(top / 6.0), 0.f);
-        const float s = e4m3_to_f32(sc);
-        uint32_t c[2] = {0u, 0u};
-        if (s != 0.f) {
-            const double inv = 1.0 / (double)s;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                c[j >> 2] |= f32x2_to_e2m1x2(to_odd(y[2 * j] * inv), to_odd(y[2 * j + 1] * inv)) << (8 * (j & 3));
+        if (R.weight) {
+            float y[16], L;
+            sure = quick_row<16>(R, src, rpos, eps, sm, lane, y, L) && quick_latent(y, L, c);
         }
-        *reinterpret_cast<uint2*>(a.c.l_data + row * kLatBytes + lane * 8) = make_uint2(c[0], c[1]);
-        a.c.l_scale[row * kLatScales + lane] = sc;
+        if (!sure) c = exact_latent(R, src, rpos, a.eps, sm, lane);
+        *reinterpret_cast<uint2*>(a.c.l_data + row * kLatBytes + lane * 8) = make_uint2(c.codes.x, c.codes.y);
+        a.c.l_scale[row * kLatScales + lane] = (uint8_t)c.scale;
     } else {
-        double y[4];
-        normed_row<4>(R, src, rpos, a.eps, sm, lane, y);
-        double top = fmax(fmax(fabs(y[0]), fabs(y[1])), fmax(fabs(y[2]), fabs(y[3])));
-        for (int o = 4; o; o >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));  // the block's 8 lanes
-        int sb = 0;
-        uint32_t c = 0;
-        if (top > 0.0) {
-            sb = ilogb(top) - 2 + 127;
-            sb = sb < 0 ? 0 : (sb > 254 ? 254 : sb);
-            const double inv = ldexp(1.0, 127 - sb);
-            c = f32x2_to_e2m1x2(to_odd(y[0] * inv), to_odd(y[1] * inv)) |
-                (f32x2_to_e2m1x2(to_odd(y[2] * inv), to_odd(y[3] * inv)) << 8);
+        if (R.weight) {
+            float y[4], L;
+            sure = quick_row<4>(R, src, rpos, eps, sm, lane, y, L) && quick_key(y, L, c);
         }
-        *reinterpret_cast<uint16_t*>(a.c.k_data + row * kLatKBytes + lane * 2) = (uint16_t)c;
-        if (!(lane & 7)) a.c.k_scale[row * kLatKScales + (lane >> 3)] = (uint8_t)sb;
+        if (!sure) c = exact_key(R, src, rpos, a.eps, sm, lane);
+        *reinterpret_cast<uint16_t*>(a.c.k_data + row * kLatKBytes + lane * 2) = (uint16_t)c.codes.x;
+        if (!(lane & 7)) a.c.k_scale[row * kLatKScales + (lane >> 3)] = (uint8_t)c.scale;
     }
 }
 
@@ -177,7 +418,7 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(PagedGatherArgs a) {
     const int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     wait_prior_grid();
     if (id >= a.rows) return;
-    const int b = (int)(id / a.n);
+    const int b = a.rows <= 0x7FFFFFFF ? (int)((uint32_t)id / (uint32_t)a.n) : (int)(id / a.n);
     const int64_t p = a.idx[id];
     int64_t row = -1;
     if (p >= 0 && p < (a.pg.max_pages << a.pg.shift)) {
@@ -226,10 +467,11 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(PagedGatherArgs a) {
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
-    const int64_t warps = (int64_t)a.batch * a.t * 3;
-    const int64_t grid = (warps + kWarps - 1) / kWarps;
+    const int64_t grid = ((int64_t)a.batch * a.t + kWarps - 1) / kWarps;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    return launch_after_prior(paged_append_kernel, dim3((unsigned)grid), dim3(32 * kWarps), 0, s, a);
+    // a kind's rows lie together: their work is alike
+    return launch_after_prior(paged_append_kernel, dim3((unsigned)grid, (unsigned)a.kinds), dim3(32 * kWarps),
+                              (size_t)16 * a.most_rot * kWarps, s, a);
 }
 
 cudaError_t launch_paged_gather(const PagedGatherArgs& a, cudaStream_t s) {

@@ -123,6 +123,42 @@ def test_append_without_norm_and_rotation_is_the_contiguous_append():
         assert torch.equal(c.swa[b], flat.swa[b])
 
 
+def test_append_of_extreme_rows():
+    """Rows whose squares leave fp32, rows of tiny and of mixed sizes, weights of any size: the 64-bit codes."""
+    t = 12
+    main, krope = _ropes(True)
+    g = _gen(12)
+    mag = torch.tensor([1.0, 3e19, 1e30, 3e38, 1e-18, 1e-25, 1e-38, 1e-40, 0.0, 1e4, 1.0, 1.0])[:, None]
+    lat = (torch.randn(1, t, 512, generator=g) * mag).clamp(-3e38, 3e38).to(torch.bfloat16)
+    key = (torch.randn(1, t, 128, generator=g) * mag).clamp(-3e38, 3e38).to(torch.bfloat16)
+    lat[0, 10, ::2] = -0.0
+    key[0, 10, ::2] = -0.0
+    lat[0, 11, ::3] *= 1e6
+    key[0, 11, ::3] *= 1e-6
+    w = (torch.randn(512, generator=g) * torch.exp2(torch.randint(-40, 40, (512,), generator=g).float())).to(torch.bfloat16)
+    w[7], w[300] = 0.0, 1e-39
+    for eps in (0.0, 1e-30, 1e-5):
+        for wl in (w, torch.ones(512, dtype=torch.bfloat16)):
+            c = _cache(1, 2, 8)
+            pos = torch.zeros(1, dtype=torch.int64, device=DEV)
+            csa.csa2_paged_append(c, 1, t, pos, lat.to(DEV), key.to(DEV), lat.to(DEV), rope=main, idx_rope=krope,
+                                  w_latent=wl.to(DEV), w_idx_k=wl[:128].to(DEV), w_swa=wl.to(DEV), eps=eps)
+            at = torch.arange(t)
+            ok = torch.ones(t, dtype=torch.bool)
+            if eps == 0.0:
+                ok[8] = False  # 0 / 0
+            eps32 = float(torch.tensor(eps, dtype=torch.float32))
+            y = _want(lat[0], wl, main, at, eps32)
+            data, scale = R.e2m1_rows(y)
+            rows = lambda plane: _logical(c, plane, 0, t).cpu()[ok]
+            assert torch.equal(rows(c.l_scale), scale[ok]) and torch.equal(rows(c.l_data), data[ok])
+            assert torch.equal(c.swa[0, :t].cpu()[ok], R.e4m3_rows(y)[ok])
+            y = _want(key[0], wl[:128], krope, at, eps32)
+            data, scale = R.mx_rows(y)
+            ok &= y.abs().amax(-1) < 2.0 ** 126
+            assert torch.equal(rows(c.k_scale), scale[ok]) and torch.equal(rows(c.k_data), data[ok])
+
+
 def test_append_of_padded_batches_strides_and_own_rotation_positions():
     B, t, page = 5, 24, 8
     main, krope = _ropes(True)
