@@ -40,7 +40,7 @@ struct PagedAppendArgs {
     double eps;
     AppendRow row[3];        // latent, indexer key, window
     int kinds, kind[3];      // those that are appended
-    int most_rot;            // channels of the widest rotation
+    int most_rot;            // channels of the widest rotation, rounded up to 4
     uint32_t* status;
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);

@@ -27,7 +27,7 @@ namespace csa2 {
 namespace {
 
 constexpr int kWarps = 4;    // per block
-constexpr int kBlocks = 12;  // per SM (registers): a row is a chain of loads, so many rows at once
+constexpr int kBlocks = 10;  // per SM (registers): a row is a chain of loads, so many rows at once
 constexpr double kInvPi = 0.31830988618379067154;
 
 // Rounding to odd: the fp32 value next to v towards zero, its last bit set unless it is v. A further
@@ -37,16 +37,13 @@ __device__ __forceinline__ float to_odd(double v) {
     return (double)f == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// A warp's shared memory: 16 bytes per rotated channel of the widest rotation (channel k of the rotated range).
+// A warp's shared memory: 8 bytes per rotated channel of the widest rotation (channel k of the rotated range).
 struct WarpMem {
     unsigned char* p;
     int rot;
     __device__ __forceinline__ float* y() const { return reinterpret_cast<float*>(p); }             // values
     __device__ __forceinline__ float* err() const { return reinterpret_cast<float*>(p) + rot; }     // and their errors
-    __device__ __forceinline__ double& xw(int k) const { return reinterpret_cast<double*>(p)[k]; }  // 64-bit rows: x * w
-    __device__ __forceinline__ double2& cs(int j) const {                                           // and cos, sin of pair j
-        return reinterpret_cast<double2*>(p + 8 * (size_t)rot)[j];
-    }
+    __device__ __forceinline__ double* wide() const { return reinterpret_cast<double*>(p); }        // values in 64 bits
 };
 
 // this lane's N channels of a row of 32 N
@@ -93,31 +90,28 @@ __device__ __forceinline__ void exact_row(const AppendRow& R, const uint16_t* sr
 #pragma unroll
     for (int i = 0; i < N; ++i)  // (exact: two bf16 factors)
         y[i] = R.weight ? (double)x[i] * (double)bf16_bits_to_f32(R.weight[lane * N + i]) : (double)x[i];
-    __syncwarp();
-    if (R.inv_freq) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int k = lane * N + i - R.offset;
-            if (k >= 0 && k < R.rot) sm.xw(k) = y[i];
-        }
+    for (int i = 0; i < N; ++i) y[i] *= r;
+    if (R.inv_freq) {
+        const int k0 = lane * N - R.offset;
+        double* const ys = sm.wide();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (k0 + i >= 0 && k0 + i < R.rot) ys[k0 + i] = y[i];
+        __syncwarp();
         for (int j = lane; j < (R.rot >> 1); j += 32) {
-            double s, c;
-            sincospi(half_turns(rpos, R.inv_freq[j]), &s, &c);
-            sm.cs(j) = make_double2(c * R.mscale, s * R.mscale);
+            double sn, cs;
+            sincospi(half_turns(rpos, R.inv_freq[j]), &sn, &cs);
+            const int2 p = pair_of(R, j);
+            const double u = ys[p.x] * R.mscale, v = ys[p.y] * R.mscale;
+            ys[p.x] = u * cs - v * sn;
+            ys[p.y] = v * cs + u * sn;
         }
         __syncwarp();
-    }
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int k = lane * N + i - R.offset;
-        y[i] *= r;
-        if (R.inv_freq && k >= 0 && k < R.rot) {
-            const int j = R.layout == CSA2_ROPE_INTERLEAVED ? k >> 1 : (k < (R.rot >> 1) ? k : k - (R.rot >> 1));
-            const int2 p = pair_of(R, j);
-            const double2 t = sm.cs(j);
-            const double z = sm.xw(k == p.x ? p.y : p.x) * r;
-            y[i] = y[i] * t.x + (k == p.x ? -z * t.y : z * t.y);
-        }
+        for (int i = 0; i < N; ++i)
+            if (k0 + i >= 0 && k0 + i < R.rot) y[i] = ys[k0 + i];
     }
 }
 
@@ -346,7 +340,7 @@ __device__ __forceinline__ bool quick_window(const float (&y)[16], float L, Code
 __global__ void __launch_bounds__(32 * kWarps, kBlocks) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-    const WarpMem sm{smem + 16 * (size_t)a.most_rot * warp, a.most_rot};
+    const WarpMem sm{smem + 8 * (size_t)a.most_rot * warp, a.most_rot};
     wait_prior_grid();  // the rows come from, and the slots may still be read by, earlier work
     const int64_t tok = (int64_t)blockIdx.x * kWarps + warp, tokens = (int64_t)a.batch * a.t;
     if (tok >= tokens) return;
@@ -471,7 +465,7 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     // a kind's rows lie together: their work is alike
     return launch_after_prior(paged_append_kernel, dim3((unsigned)grid, (unsigned)a.kinds), dim3(32 * kWarps),
-                              (size_t)16 * a.most_rot * kWarps, s, a);
+                              (size_t)8 * a.most_rot * kWarps, s, a);
 }
 
 cudaError_t launch_paged_gather(const PagedGatherArgs& a, cudaStream_t s) {
