@@ -146,16 +146,37 @@ __device__ __forceinline__ void store_out(const Fp8GemmArgs& a, int64_t i, int64
         reinterpret_cast<uint16_t*>(a.out)[i * a.out_stride + j] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// two fp32 as the 64-bit operand of the packed instructions, and back (in instructions of their own: shifts of
+// a 64-bit sum make the compiler keep it as two registers and pack it again for every product)
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+// acc (two fp32) += v * s, element by element
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t s) {
+    asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(acc) : "r"(v0), "r"(v1), "l"(s));
+}
+
 // Tiles of 128 weight rows (the MMA's M: a lane of tensor memory per output column) x NT rows of x.
 // The weights' scale of a block is then one number per tile, the rows' scales are along the
-// registers of a thread. Warp 0 copies, warp 1 issues the MMAs, warps 2 .. 5 scale and add. The
-// blocks of the contraction are split over the a cluster's CTAs; their sums meet in shared memory and
+// registers of a thread. Warp 0 copies, warp 1 issues the MMAs, the others scale and add: four of them (one
+// per quarter of tensor memory's lanes), or eight for 64 columns (half the columns each). The
+// blocks of the contraction are split over a cluster's CTAs; their sums meet in shared memory and
 // are added in rank order.
 template <int NT>
 struct Cols {
-    static constexpr int kThreads = 192;
+    static constexpr int kParts = NT >= 64 ? 2 : 1;               // warps per quarter of the lanes
+    static constexpr int kCols = NT / kParts;                     // columns (and fp32 sums) of a thread
+    static constexpr int kReaders = 128 * kParts;
+    static constexpr int kThreads = 64 + kReaders;
     static constexpr int kStage = 128 * 128 + NT * 128;
-    static constexpr int kStages = NT <= 32 ? 5 : (NT == 64 ? 4 : 3);
+    static constexpr int kStages = NT <= 32 ? 5 : 4;
     static constexpr uint32_t kTmem = 2 * NT < 32 ? 32 : 2 * NT;  // two accumulators
     static constexpr int kJoin = NT * 128 * 4;                    // this CTA's sums for the join
     static constexpr int kData = kStages * kStage > kJoin ? kStages * kStage : kJoin;
@@ -163,8 +184,8 @@ struct Cols {
 };
 
 template <int NT>
-__global__ void __launch_bounds__(192) fp8_cols_kernel(Fp8GemmArgs a, const __grid_constant__ CUtensorMap wmap,
-                                                       const __grid_constant__ CUtensorMap xmap, int split) {
+__global__ void __launch_bounds__(Cols<NT>::kThreads, 2)
+fp8_cols_kernel(Fp8GemmArgs a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, int split) {
     using G = Cols<NT>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -188,7 +209,7 @@ __global__ void __launch_bounds__(192) fp8_cols_kernel(Fp8GemmArgs a, const __gr
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], 128);
+            mbar_init(&tempty[i], G::kReaders / 32);
         }
         mbar_fence_init();
         prefetch_tmap(&wmap);
@@ -237,62 +258,71 @@ __global__ void __launch_bounds__(192) fp8_cols_kernel(Fp8GemmArgs a, const __gr
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     mma_f8(tb + buf * NT, sw128_desc(ad + 32 * q), sw128_desc(bd + 32 * q), f8_idesc(128, NT), q > 0);
-                mma_commit(&empty[st]);
                 mma_commit(&tfull[buf]);
+                mma_commit(&empty[st]);
             }
         }
         __syncwarp();
     } else {
-        const int et = tid - 64;        // 0 .. 127
-        const int quad = warp & 3;      // the tensor-memory lanes this warp may read
-        const int64_t row = m0 + et;    // the row of x whose scales this thread fetches
-        float acc[NT];
+        const int et = tid - 64;          // 0 .. kReaders - 1
+        const int quad = warp & 3;        // the tensor-memory lanes this warp may read
+        const int col0 = G::kParts == 2 ? (warp - 2) / 4 * G::kCols : 0;
+        // this thread's row of x, whose scales it fetches (two blocks ahead: nothing waits for them)
+        const bool mine = et < NT && m0 + et < a.m;
+        const float* xs = a.xs + (int64_t)b0 * a.m + (mine ? m0 + et : 0);
+        const float* ws = a.ws + (n0 >> 7) * nb;
+        uint64_t acc[G::kCols / 2];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) acc[i] = 0.f;
-        auto fetch = [&](int b) {
-            return (b < b1 && et < NT && row < a.m)
-                       ? __ldg(a.xs + (int64_t)b * a.m + row) * __ldg(a.ws + (n0 >> 7) * nb + b) : 0.f;
-        };
-        float s0 = fetch(b0), s1 = fetch(b0 + 1);
+        for (int i = 0; i < G::kCols / 2; ++i) acc[i] = 0ull;
+        float x0 = __ldg(xs), w0 = __ldg(ws + b0), x1 = 0.f, w1 = 0.f;
+        if (b0 + 1 < b1) {
+            x1 = __ldg(xs += a.m);
+            w1 = __ldg(ws + b0 + 1);
+        }
         for (int b = b0, i = 0; b < b1; ++b, ++i) {
             const int buf = i & 1;
-            if (et < NT) sc[buf * NT + et] = s0;
-            s0 = s1;
-            s1 = fetch(b + 2);
+            float x2 = 0.f, w2 = 0.f;
+            if (b + 2 < b1) {
+                x2 = __ldg(xs += a.m);
+                w2 = __ldg(ws + b + 2);
+            }
+            if (et < NT) sc[buf * NT + et] = mine ? x0 * w0 : 0.f;
+            x0 = x1, w0 = w1, x1 = x2, w1 = w2;
+            asm volatile("bar.sync 1, %0;" ::"n"(G::kReaders) : "memory");  // the scales of block b (and b - 1 is read)
             wait(&tfull[buf], (i >> 1) & 1);
-            asm volatile("bar.sync 1, 128;" ::: "memory");  // the scales of block b (and b - 1 is read)
             tc_fence_after();
-            constexpr int W = NT < 32 ? 16 : 32;
+            constexpr int W = G::kCols < 32 ? 16 : 32;
+            const uint32_t at = tb + ((uint32_t)(32 * quad) << 16) + buf * NT + col0;
+            const float* s = sc + buf * NT + col0;
 #pragma unroll
-            for (int c = 0; c < NT; c += W) {
+            for (int c = 0; c < G::kCols; c += W) {
                 uint32_t v[W];
-                const uint32_t at = tb + ((uint32_t)(32 * quad) << 16) + buf * NT + c;
-                if constexpr (W == 32) tmem_ld32(at, v); else tmem_ld16(at, v);
+                if constexpr (W == 32) tmem_ld32(at + c, v); else tmem_ld16(at + c, v);
                 tmem_ld_done(v);
+                if (c + W == G::kCols) {  // the last part is in registers: the accumulator may be written again
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tempty[buf]);
+                }
 #pragma unroll
                 for (int j = 0; j < W; j += 4) {
-                    const float4 s = *reinterpret_cast<const float4*>(sc + buf * NT + c + j);
-                    acc[c + j] = fmaf(__uint_as_float(v[j]), s.x, acc[c + j]);
-                    acc[c + j + 1] = fmaf(__uint_as_float(v[j + 1]), s.y, acc[c + j + 1]);
-                    acc[c + j + 2] = fmaf(__uint_as_float(v[j + 2]), s.z, acc[c + j + 2]);
-                    acc[c + j + 3] = fmaf(__uint_as_float(v[j + 3]), s.w, acc[c + j + 3]);
+                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(s + c + j);
+                    fma2(acc[(c + j) / 2], v[j], v[j + 1], f.x);
+                    fma2(acc[(c + j) / 2 + 1], v[j + 2], v[j + 3], f.y);
                 }
             }
-            tc_fence_before();
-            mbar_arrive(&tempty[buf]);
         }
         const int n = 32 * quad + lane;
-        if (split == 1) {
-            if (n0 + n < a.n) {
+        // every copy of this CTA has landed and been read: with a split the stages become the sums [NT][128]
+        float* part = reinterpret_cast<float*>(sm);
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    if (m0 + i < a.m) store_out(a, m0 + i, n0 + n, acc[i]);
-            }
-        } else {
-            // every copy of this CTA has landed and been read: the stages become the sums [NT][128]
-            float* part = reinterpret_cast<float*>(sm);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) part[i * 128 + n] = acc[i];
+        for (int i = 0; i < G::kCols; ++i) {
+            const float2 x = unpack2(acc[i / 2]);
+            const float v = i & 1 ? x.y : x.x;
+            if (split > 1)
+                part[(col0 + i) * 128 + n] = v;
+            else if (n0 + n < a.n && m0 + col0 + i < a.m)
+                store_out(a, m0 + col0 + i, n0 + n, v);
         }
     }
     if (split > 1) {
@@ -314,124 +344,86 @@ __global__ void __launch_bounds__(192) fp8_cols_kernel(Fp8GemmArgs a, const __gr
     if (warp == 1) tmem_dealloc(tb, G::kTmem);
 }
 
-// ---- large products: a pair of CTAs per tile ------------------------------------------------------------
+// ---- large products: rows of x on the lanes --------------------------------------------------------------
 //
-// Tiles of 256 rows of x x 256 weight rows, one per cluster of two CTAs (cta_group::2: each CTA stages its
-// 128 rows of x and 128 of the weights, and holds its 128 rows' sums in tensor memory, so a stage's 32 KB
-// feed twice the products that one CTA's 48 KB would). Here a lane of tensor memory is a row of x: the
-// row's scale of a block is one number per thread. Persistent: each pair takes tiles in turn, rows
-// fastest, so that the pairs at work share weight rows in L2.
-// Warp 0 copies, warp 1 of the even CTA issues the MMAs for both, warps 4 .. 11 scale and add (two per
-// quarter of the lanes, 128 columns and 128 fp32 sums a thread). Two accumulators of 256 columns
-// alternate block by block: while the tensor cores write one, the other is read. Four of 128 columns, or
-// 16 reading warps, cost more in barriers than they hide (917 and 701 us where this takes 595, for
-// 4096 x 4096 x 32768).
-constexpr int kPairThreads = 384, kPairStages = 6, kPairStage = 2 * 128 * 128;
-constexpr int kPairSmem = kPairStages * kPairStage + (2 * kPairStages + 4) * 8 + 16 + 1024;
+// Tiles of 128 rows of x x 256 weight rows. A lane of tensor memory is a row of x: the row's scale of a
+// block is one number per thread. Persistent: each CTA takes tiles in turn, rows fastest, so that those at
+// work share weight rows in L2.
+// Warp 0 copies, warp 1 issues the MMAs, warps 4 .. 11 scale and add (two per quarter of the lanes, 128
+// columns and 128 fp32 sums a thread). Two accumulators of 256 columns alternate block by block: while the
+// tensor cores write one, the other is read. The reading bounds it: without the products of the scales the
+// rest of the kernel takes 420 us where the whole takes 565 (4096 x 4096 x 32768, 1.95 PFLOP/s). Tried and
+// slower there: 16 reading warps (700 us), four accumulators of 128 columns (917), pairs of CTAs sharing
+// the weights (cta_group::2: 571, and 45 against 28 for 128 rows).
+// The tile leaves through shared memory, so that a warp's stores are whole lines of a row at any alignment.
+constexpr int kRowsThreads = 384;
 // registers at launch: 168 x 384; the copying warpgroup gives up 112, the two others take 56 each
-constexpr uint32_t kPairRegsFew = 56, kPairRegsMany = 224;
+constexpr uint32_t kRegsFew = 56, kRegsMany = 224;
+constexpr int kRowsStage = 128 * 128 + 256 * 128, kRowsStages = 4;
+constexpr int kRowsOut = 8 * 32 * 33 * 4;  // per reading warp: 32 rows of 32 words, rows one bank apart
+constexpr int kRowsSmem = kRowsStages * kRowsStage + kRowsOut + (2 * kRowsStages + 4) * 8 + 16 + 1024;
 
-__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, bool acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"((uint32_t)acc)
-        : "memory");
-}
-// one arrival on the barrier at this address in both CTAs once every MMA issued before has completed
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
-}
-__device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    return a;
-}
-// (no cluster-wide release: what it orders are tensor-memory reads, which the tcgen05 fences order; a
-// release over the cluster is a memory barrier, which the readers spent half their time in)
-__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-// a box into this CTA's shared memory, counted on a barrier of the pair (an address in the cluster)
-__device__ __forceinline__ void tma_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
-}
-// acc (two fp32) += v * s, element by element
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t s) {
-    asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(acc) : "r"(v0), "r"(v1), "l"(s));
-}
-
-// 32 of a row's sums to out[row][col ..]
-__device__ __forceinline__ void store32(const Fp8GemmArgs& a, int64_t row, int64_t col, const uint64_t* acc, bool wide) {
-    float v[32];
+// The warp's 32 rows (row0 + lane), 32 words each in its buffer (row r at 33 r; a word one fp32 or two bf16
+// columns from col on), to out. wide: every row starts on 16 bytes.
+__device__ __forceinline__ void store_words(const Fp8GemmArgs& a, const uint32_t* b, int64_t row0, int64_t col, bool wide,
+                                            int lane) {
+    __syncwarp();
+    const int per = a.out_f32 ? 1 : 2;  // columns of a word
+    const int rows = a.m - row0 < 32 ? (int)(a.m - row0) : 32;
+    if (wide && col + 32 * per <= a.n) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        v[2 * i] = __uint_as_float((uint32_t)acc[i]);
-        v[2 * i + 1] = __uint_as_float((uint32_t)(acc[i] >> 32));
-    }
-    if (wide && col + 32 <= a.n) {
-        if (a.out_f32) {
-            float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + row * a.out_stride + col);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else {
-            uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + row * a.out_stride + col);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
-                    w[j] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-                d[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3), c = 4 * (lane & 7);
+            const uint4 v = make_uint4(b[r * 33 + c], b[r * 33 + c + 1], b[r * 33 + c + 2], b[r * 33 + c + 3]);
+            if (r < rows)
+                *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(a.out) +
+                                          ((row0 + r) * a.out_stride + col + per * c) * (4 / per)) = v;
         }
+    } else if (a.out_f32) {
+        for (int r = 0; r < rows; ++r)
+            if (col + lane < a.n)
+                reinterpret_cast<uint32_t*>(a.out)[(row0 + r) * a.out_stride + col + lane] = b[r * 33 + lane];
     } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (col + i < a.n) store_out(a, row, col + i, v[i]);
+        for (int r = 0; r < rows; ++r) {
+            const uint32_t v = b[r * 33 + lane];
+            uint16_t* d = reinterpret_cast<uint16_t*>(a.out) + (row0 + r) * a.out_stride + col + 2 * lane;
+            if (col + 2 * lane < a.n) d[0] = (uint16_t)v;
+            if (col + 2 * lane + 1 < a.n) d[1] = (uint16_t)(v >> 16);
+        }
     }
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-fp8_pair_kernel(Fp8GemmArgs a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                int64_t mt, int64_t tiles) {
+__global__ void __launch_bounds__(kRowsThreads, 1)
+fp8_rows_gemm_kernel(Fp8GemmArgs a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                     int mt, int tiles) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + kPairStages * kPairStage);  // the even CTA's counts both CTAs' copies
-    uint64_t* empty = full + kPairStages;
-    uint64_t* tfull = empty + kPairStages;
-    uint64_t* tempty = tfull + 2;  // the even CTA's: both CTAs' warps
+    float* outs = reinterpret_cast<float*>(sm + kRowsStages * kRowsStage);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + kRowsStages * kRowsStage + kRowsOut);
+    uint64_t* empty = full + kRowsStages;
+    uint64_t* tfull = empty + kRowsStages;
+    uint64_t* tempty = tfull + 2;
     uint32_t* slot = reinterpret_cast<uint32_t*>(tempty + 2);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = cluster_rank();
-    const int64_t pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const int step = (int)gridDim.x, first = (int)blockIdx.x;
     const int nb = (a.k + 127) / 128;
 
     if (tid == 0) {
-        for (int i = 0; i < kPairStages; ++i) {
+        for (int i = 0; i < kRowsStages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], 16);
+            mbar_init(&tempty[i], 8);
         }
         mbar_fence_init();
         prefetch_tmap(&wmap);
         prefetch_tmap(&xmap);
     }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(slot)) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    }
+    if (warp == 1) tmem_alloc(slot, 512);
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // both CTAs' barriers and tensor memory are there
     tc_fence_after();
     const uint32_t tb = *slot;
     wait_prior_grid();
@@ -445,122 +437,133 @@ fp8_pair_kernel(Fp8GemmArgs a, const __grid_constant__ CUtensorMap wmap, const _
     };
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegsFew));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
         int st = 0;
         uint32_t ph = 0;  // the stage in turn and how often (parity) the ring has gone round
         auto next = [&]() {
-            if (++st == kPairStages) {
+            if (++st == kRowsStages) {
                 st = 0;
                 ph ^= 1u;
             }
         };
         if (warp == 0 && lane == 0) {
-            for (int64_t t = pair; t < tiles && ok; t += pairs) {
-                const int m0 = (int)(t % mt * 256 + 128 * rank), n0 = (int)(t / mt * 256 + 128 * rank);
+            for (int t = first; t < tiles && ok; t += step) {
+                const int m0 = (int)(t % mt * 128), n0 = (int)(t / mt * 256);
                 for (int b = 0; b < nb; ++b) {
                     if (!wait(&empty[st], ph ^ 1u)) break;  // (passes at once in the first round)
-                    unsigned char* d = sm + st * kPairStage;
-                    if (rank == 0) mbar_expect_tx(&full[st], 2 * kPairStage);
-                    const uint32_t bar = at_rank(&full[st], 0);
-                    tma_2d_pair(d, &xmap, b * 128, m0, bar);
-                    tma_2d_pair(d + 128 * 128, &wmap, b * 128, n0, bar);
+                    unsigned char* d = sm + st * kRowsStage;
+                    mbar_expect_tx(&full[st], kRowsStage);
+                    tma_2d_g2s(d, &xmap, b * 128, m0, &full[st]);
+                    tma_2d_g2s(d + 128 * 128, &wmap, b * 128, n0, &full[st]);
+                    tma_2d_g2s(d + 2 * 128 * 128, &wmap, b * 128, n0 + 128, &full[st]);
                     next();
                 }
             }
             // every stage is read (its last commit has arrived) before this CTA may end
-            for (int j = 0; j < kPairStages; ++j) {
+            for (int j = 0; j < kRowsStages; ++j) {
                 mbar_wait(&empty[st], ph ^ 1u, kWaitNs);
                 next();
             }
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && lane == 0) {
             uint32_t i = 0;  // accumulators written so far
-            for (int64_t t = pair; t < tiles && ok; t += pairs) {
-                for (int b = 0; b < nb && ok; ++b) {
-                    if (!wait(&full[st], ph)) break;
-                    const uint32_t ad = smem_u32(sm + st * kPairStage), bd = ad + 128 * 128;
+            for (int t = first; t < tiles && ok; t += step) {
+                for (int b = 0; b < nb && ok; ++b, ++i) {
                     const uint32_t buf = i & 1u;
-                    if (!wait(&tempty[buf], ((i >> 1) & 1u) ^ 1u)) break;
+                    if (!wait(&full[st], ph) || !wait(&tempty[buf], ((i >> 1) & 1u) ^ 1u)) break;
                     tc_fence_after();
+                    const uint32_t ad = smem_u32(sm + st * kRowsStage), bd = ad + 128 * 128;
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        mma_f8_pair(tb + buf * 256, sw128_desc(ad + 32 * q), sw128_desc(bd + 32 * q), f8_idesc(256, 256), q > 0);
-                    commit_pair(&tfull[buf]);
-                    commit_pair(&empty[st]);
-                    ++i;
+                        mma_f8(tb + buf * 256, sw128_desc(ad + 32 * q), sw128_desc(bd + 32 * q), f8_idesc(128, 256), q > 0);
+                    mma_commit(&tfull[buf]);
+                    mma_commit(&empty[st]);
                     next();
                 }
             }
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairRegsMany));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
         const int quad = warp & 3, part = (warp - 4) >> 2;
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-        // 16-byte stores where every row starts on 16 bytes
-        const int per16 = a.out_f32 ? 4 : 8;
-        const bool wide = ((uintptr_t)a.out & 15) == 0 && a.out_stride % per16 == 0;
-        const uint32_t peer = at_rank(&tempty[0], 0);
         uint32_t i = 0;
-        for (int64_t t = pair; t < tiles; t += pairs) {
-            const int64_t row = t % mt * 256 + 128 * rank + 32 * quad + lane;
-            const int64_t col = t / mt * 256 + 128 * part;
-            // the scales of the next two blocks are on their way (their product is formed when they are used,
-            // so that nothing waits for them before)
+        for (int t = first; t < tiles; t += step) {
+            const int row0 = t % mt * 128 + 32 * quad, row = row0 + lane;
+            const int col = t / mt * 256 + 128 * part;  // (below 2^31: the padded sizes are checked at launch)
+            // the next block's scales are on their way (their product is formed when they are used, so that
+            // nothing waits for them before)
             const bool live = row < a.m && col < a.n;
             const float* xs = a.xs + (live ? row : 0);
             const float* ws = a.ws + (live ? (col >> 7) * nb : 0);
-            const int64_t xstep = a.m;
             uint64_t acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0ull;
-            float x0 = __ldg(xs), w0 = __ldg(ws), x1 = 0.f, w1 = 0.f;
-            if (nb > 1) {
-                x1 = __ldg(xs += xstep);
-                w1 = __ldg(ws + 1);
-            }
+            float x0 = __ldg(xs), w0 = __ldg(ws);
             for (int b = 0; b < nb; ++b, ++i) {
-                float x2 = 0.f, w2 = 0.f;
-                if (b + 2 < nb) {
-                    x2 = __ldg(xs += xstep);
-                    w2 = __ldg(ws + b + 2);
-                }
                 const float f = x0 * w0;
-                const uint64_t s = ((uint64_t)__float_as_uint(f) << 32) | __float_as_uint(f);
-                x0 = x1, w0 = w1, x1 = x2, w1 = w2;
+                const uint64_t s = pack2(f, f);
+                if (b + 1 < nb) {
+                    x0 = __ldg(xs += a.m);
+                    w0 = __ldg(ws + b + 1);
+                }
                 const uint32_t buf = i & 1u;
                 wait(&tfull[buf], (i >> 1) & 1u);
                 tc_fence_after();
                 const uint32_t at = tb + lanes + buf * 256 + 128 * part;
-                constexpr int W = 32;
-                uint32_t v[2][W];
+                uint32_t v[2][32];
                 tmem_ld32(at, v[0]);
                 tmem_ld_done(v[0]);
 #pragma unroll
-                for (int c = 0; c < 128 / W; ++c) {
-                    if (c + 1 < 128 / W) tmem_ld32(at + W * (c + 1), v[(c + 1) & 1]);
+                for (int c = 0; c < 4; ++c) {
+                    if (c < 3) tmem_ld32(at + 32 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
-                    for (int j = 0; j < W / 2; ++j) fma2(acc[W / 2 * c + j], v[c & 1][2 * j], v[c & 1][2 * j + 1], s);
-                    if (c + 1 < 128 / W) tmem_ld_done(v[(c + 1) & 1]);
-                    if (c + 2 == 128 / W) {  // the last part is in registers: the accumulator may be written again
+                    for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], v[c & 1][2 * j], v[c & 1][2 * j + 1], s);
+                    if (c < 3) tmem_ld_done(v[(c + 1) & 1]);
+                    if (c == 2) {  // the last part is in registers: the accumulator may be written again
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) {
-                            if (rank == 0) mbar_arrive(&tempty[buf]); else arrive_at(peer + 8 * buf);
-                        }
+                        if (lane == 0) mbar_arrive(&tempty[buf]);
                     }
                 }
             }
-            if (row < a.m) {
+            if (row0 < a.m && col < a.n) {
+                // (the words leave the registers one by one: no copy of them is live beside the sums)
+                uint32_t* buffer = reinterpret_cast<uint32_t*>(outs) + (warp - 4) * 32 * 33;
+                // 16-byte stores where every row starts on 16 bytes
+                const bool wide = ((uintptr_t)a.out & 15) == 0 && a.out_stride % (a.out_f32 ? 4 : 8) == 0;
+                if (a.out_f32) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) store32(a, row, col + 32 * c, acc + 16 * c, wide);
+                    for (int c = 0; c < 4; ++c) {
+                        __syncwarp();  // the words before are read
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 x = unpack2(acc[16 * c + j]);
+                            buffer[lane * 33 + 2 * j] = __float_as_uint(x.x);
+                            buffer[lane * 33 + 2 * j + 1] = __float_as_uint(x.y);
+                        }
+                        store_words(a, buffer, row0, col + 32 * c, wide, lane);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float2 x = unpack2(acc[32 * c + j]);
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+                            buffer[lane * 33 + j] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                        store_words(a, buffer, row0, col + 64 * c, wide, lane);
+                    }
+                }
             }
         }
     }
     __syncwarp();
     tc_fence_before();
-    cluster_sync();  // no CTA ends while the other's MMAs or arrivals may reach it
+    __syncthreads();
     tc_fence_after();
-    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tb) : "memory");
+    if (warp == 1) tmem_dealloc(tb, 512);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -592,6 +595,14 @@ cudaError_t make_map(CUtensorMap* map, const uint8_t* p, int64_t rows, int k, in
                ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// The contraction split (by 2, 4 or 8), two blocks each at least: to about one CTA an SM, and up to two in
+// clusters of 4 at most (64 tiles of 32 blocks: 14.5 us by 2, 12.6 by 4; 32 tiles: 7.5 us by 4, 8.2 by 8).
+int cols_split(int64_t tiles, int nb) {
+    int split = 1;
+    while (split < 8 && nb >= split * 4 && tiles * split * 2 <= (split < 4 ? 296 : 160)) split *= 2;
+    return split;
+}
+
 template <int NT>
 cudaError_t launch_cols(const Fp8GemmArgs& a, cudaStream_t s) {
     using G = Cols<NT>;
@@ -603,27 +614,25 @@ cudaError_t launch_cols(const Fp8GemmArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int64_t tiles = ((a.n + 127) / 128) * ((a.m + NT - 1) / NT);
     const int nb = (a.k + 127) / 128;
-    // the contraction split (by 2, 4 or 8) while that still gives about one CTA per SM, two blocks each
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= 160 && nb >= split * 4) split *= 2;
+    const int split = cols_split(tiles, nb);
     if (tiles * split > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     return launch_cluster(k, dim3((unsigned)(tiles * split)), dim3(G::kThreads), split, G::kSmem, s, a, wmap, xmap, split);
 }
 
-cudaError_t launch_pair(const Fp8GemmArgs& a, cudaStream_t s) {
+cudaError_t launch_rows_gemm(const Fp8GemmArgs& a, cudaStream_t s) {
     CUtensorMap wmap, xmap;
     cudaError_t e = make_map(&wmap, a.w, a.n, a.k, 128);
     if (e == cudaSuccess) e = make_map(&xmap, a.x, a.m, a.k, 128);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+        e = cudaFuncSetAttribute(fp8_rows_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
     int dev = 0, sms = 0;
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const int64_t mt = (a.m + 255) / 256, tiles = mt * ((a.n + 255) / 256);
-    const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
-    return launch_after_prior(fp8_pair_kernel, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), kPairSmem, s, a, wmap,
-                              xmap, mt, tiles);
+    const int64_t mt = (a.m + 127) / 128, tiles = mt * ((a.n + 255) / 256);
+    if (tiles > 0x3FFFFFFF || a.m > 0x7FFFFE00 || a.n > 0x7FFFFE00) return cudaErrorInvalidConfiguration;
+    return launch_after_prior(fp8_rows_gemm_kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kRowsThreads),
+                              kRowsSmem, s, a, wmap, xmap, (int)mt, (int)tiles);
 }
 
 }  // namespace
@@ -652,9 +661,15 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t s) {
     if (a.m <= 16) return launch_cols<16>(a, s);
     if (a.m <= 32) return launch_cols<32>(a, s);
     if (a.m <= 64) return launch_cols<64>(a, s);
-    const int64_t tiles = ((a.m + 255) / 256) * ((a.n + 255) / 256);
-    if (a.m > 128 && tiles >= 37) return launch_pair(a, s);
-    return launch_cols<128>(a, s);
+    // Both kernels' time goes by the blocks that a CTA takes one after the other: 0.53 us a block with rows of x
+    // along the columns (two CTAs an SM, 64 rows each, the contraction split for few tiles), 0.57 us with
+    // them on the lanes (one CTA an SM, 128 rows x 256). Measured (us, columns / lanes): 128 x 2112 x 7168
+    // 13.7 / 34, 256 x 4096 x 4096 17.8 / 20, 777 x 4099 x 4112 47 / 26, 128 x 32768 x 4096 44 / 28.
+    const int nb = (a.k + 127) / 128;
+    const int64_t tc = ((a.n + 127) / 128) * ((a.m + 63) / 64), tr = ((a.n + 255) / 256) * ((a.m + 127) / 128);
+    const int split = cols_split(tc, nb);
+    const int64_t cols = (tc * split + 295) / 296 * ((nb + split - 1) / split), rows = (tr + 147) / 148 * nb;
+    return cols * 53 <= rows * 57 ? launch_cols<64>(a, s) : launch_rows_gemm(a, s);
 }
 
 }  // namespace csa2
