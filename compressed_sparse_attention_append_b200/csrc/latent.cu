@@ -28,10 +28,11 @@
 //   4. O^T += L^T P^T on tcgen05 (M = 128 channels, four M tiles, N = 64 heads, K = 128 keys): the
 //      same shared-memory bytes of L, read MN-major (channels contiguous), so the latent is
 //      dequantised once for both products.
-// The two channel halves of L (64-channel blocks 0..3 and 4..7) are dequantised by separate halves
-// of the CTA, each as soon as the O^T MMAs of the previous tile that read it have completed, and the
+// The two channel halves of L (64-channel blocks 0..3 and 4..7) are dequantised one after the other,
+// each as soon as the O^T MMAs of the previous tile that read it have completed, and the
 // S^T k-steps of a half are issued as soon as that half is in place (mbarriers between the threads
-// and the MMA issuer), so dequantisation overlaps the tensor pipe. The row's indices are checked
+// and the MMA issuer), so dequantisation overlaps the tensor pipe. Four lanes take a key, 16 bytes each of
+// every 64 of its row: a warp's load touches 8 lines, not 32. The row's indices are checked
 // and staged in shared memory once, so no tile waits on a dependent index load.
 // Tensor memory: S^T in columns 0..63, O^T in columns 64..319 (channels on the lanes).
 // The result is normalised by the per-head sum of P at the end: out = O / l, lse = m ln 2 + ln l.
@@ -45,7 +46,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kT = 512;                       // threads: key = tid & 127, channels 128 (tid >> 7) .. +127
+constexpr int kT = 512;                       // threads; loads: key tid >> 2, a quarter of its chunks each
 constexpr int kTile = 128;                    // keys per tile (MMA M of S^T)
 constexpr int kBlk = kTile * 128;             // 16384: one 64-channel block of the L tile
 constexpr int kLTile = 8 * kBlk;              // 131072: the fp16 L tile
@@ -145,12 +146,14 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + kOffSlot);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int key = tid & 127, qq = tid >> 7;      // load / dequantise: key, channels 128 qq ..
-    const int half = qq >> 1;                      // channel half (blocks 4 half .. 4 half + 3)
+    const int lkey = tid >> 2, qq = tid & 3;       // load / dequantise: key of the tile, 16-byte chunks 4 c + qq of its row
+    const int key = tid & 127;                     // softmax: key (tensor-memory lane 32 quad + lane)
     const int quad = warp & 3, cg = warp >> 2;     // softmax / epilogue: lanes 32 quad .., heads 16 cg ..
     const int split = PAGED ? a.split : 1;
     const int rank = PAGED && split > 1 ? (int)cluster_rank() : 0;
     const int row = PAGED ? (int)(blockIdx.x / (unsigned)split) : (int)blockIdx.x, K = a.k;
+    // (takes some 3500 cycles: under way while the other warps fetch the row's position and indices)
+    if (warp == kT / 32 - 1) tmem_alloc(tslot, kCols);
     wait_prior_grid();  // indices, cache and queries come from earlier work on the stream
 
     const int b = row / a.tq;
@@ -178,19 +181,18 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
         mbar_init(&bars[kBarS], 1);
         mbar_init(&bars[kBarO0], 1);
         mbar_init(&bars[kBarO1], 1);
-        mbar_init(&bars[kBarH0], kT / 2);
-        mbar_init(&bars[kBarH1], kT / 2);
+        mbar_init(&bars[kBarH0], kT);
+        mbar_init(&bars[kBarH1], kT);
         mbar_fence_init();
     }
     if (tid < 64) s_m[tid] = -INFINITY;
-    if (warp == 0) tmem_alloc(tslot, kCols);
-    // Q (this thread: head tid >> 3, channels 64 (tid & 7) ..) requested first; it is converted once
+    // Q (this thread: 16-byte chunks tid + 512 c of the row's 4096) requested first; it is converted once
     // the row's indices are staged and tile 0's rows requested, so that the three loads overlap
     uint4 qv[8];
     {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)row * kLatHQ + (tid >> 3)) * kLatD + 64 * (tid & 7));
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)row * kLatHQ * kLatD) + tid;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) qv[c] = __ldg(src + c);
+        for (int c = 0; c < 8; ++c) qv[c] = __ldg(src + kT * c);
     }
     // the row's indices, checked once (an entry that is -1, not visible or out of range becomes -1)
     const int i0 = PAGED ? t0 * kTile : 0, i1 = PAGED && (t0 + nt) * kTile < K ? (t0 + nt) * kTile : K;
@@ -217,74 +219,71 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
         }
     };
 
-    // this thread's window row (key `key` of the window tile), channels 128 qq ..
+    // this thread's chunks of its window row (16 channels: 16 qq .. of 64-channel block i in chunk 4 i)
     auto win_src = [&]() {
-        const int64_t p = lo + key;
-        return reinterpret_cast<const uint4*>(a.c.swa + (swa_row0 + (size_t)(p & (a.c.swa_cap - 1))) * kLatSwa +
-                                              128 * qq);
+        const int64_t p = lo + lkey;
+        return reinterpret_cast<const uint4*>(a.c.swa + (swa_row0 + (size_t)(p & (a.c.swa_cap - 1))) * kLatSwa) + qq;
     };
-    // ---- raw rows of tile j into registers (this thread: key `key`, channels 128 qq .. +127) ----
-    // (of a window row only the first 64 channels: the other 64 are loaded while it is dequantised,
-    // so that no more than 18 registers of raw data stay live across the softmax of the tile before)
+    // ---- raw rows of tile j into registers (this thread: key lkey, of each 128 channels c the 32 from 32 qq on) ----
+    // (of a window row only the first channel half: the other is loaded while it is dequantised, so that no
+    // more than 18 registers of raw data stay live across the softmax of the tile before)
     uint4 raw[4];
-    uint2 rsc;
-    bool kvalid = false;  // the key of this thread in the tile being loaded
+    uint32_t rsc[2];  // two scales per c
     auto load_tile = [&](int j) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-        rsc = make_uint2(0, 0);
-        kvalid = false;
+        rsc[0] = rsc[1] = 0u;
         if (j < nt && t0 + j < ft) {  // (the indices of this CTA's tiles are staged, no others)
-            const int i = (t0 + j) * kTile + key;
+            const int i = (t0 + j) * kTile + lkey;
             const int v = i < K ? sidx[i] : -1;
             if (v >= 0) {
-                kvalid = true;
-                const uint4* src = reinterpret_cast<const uint4*>(a.c.l_data + (seq_row0 + (size_t)v) * kLatBytes + 64 * qq);
+                const uint4* src = reinterpret_cast<const uint4*>(a.c.l_data + (seq_row0 + (size_t)v) * kLatBytes) + qq;
+                const uint16_t* sc = reinterpret_cast<const uint16_t*>(a.c.l_scale + (seq_row0 + (size_t)v) * kLatScales) + qq;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) raw[c] = __ldg(src + c);
-                rsc = __ldg(reinterpret_cast<const uint2*>(a.c.l_scale + (seq_row0 + (size_t)v) * kLatScales + 8 * qq));
+                for (int c = 0; c < 4; ++c) raw[c] = __ldg(src + 4 * c);
+                rsc[0] = (uint32_t)__ldg(sc) | ((uint32_t)__ldg(sc + 4) << 16);
+                rsc[1] = (uint32_t)__ldg(sc + 8) | ((uint32_t)__ldg(sc + 12) << 16);
             }
-        } else if (j < nt && key < nwin) {
-            kvalid = true;
+        } else if (j < nt && lkey < nwin) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) raw[c] = __ldg(win_src() + c);  // channels 128 qq .. +63
+            for (int c = 0; c < 4; ++c) raw[c] = __ldg(win_src() + 4 * c);
         }
     };
-    // dequantise the registers into the L tile: channel 128 qq + 8 c lands in 64-channel block
-    // 2 qq + c / 8, chunk c % 8, of row `key`
-    auto dequant = [&](bool fp4, bool kvalid_dq) {
+    // whether this thread's softmax key counts in tile j
+    auto key_valid = [&](int j) {
+        const int i = (t0 + j) * kTile + key;
+        return t0 + j < ft ? i < K && sidx[i] >= 0 : key < nwin;
+    };
+    // channel half hh of the registers into the L tile (8-channel chunks of row lkey in its 64-channel blocks)
+    auto dequant = [&](int hh, bool fp4, bool more) {
         if (fp4) {
 #pragma unroll
-            for (int bk = 0; bk < 8; ++bk) {  // 16-channel scale block bk: code words 2 bk, 2 bk + 1
-                const uint32_t s2 = scale_h2(((bk < 4 ? rsc.x : rsc.y) >> (8 * (bk & 3))) & 0xFFu);
-                const uint4 rw = raw[bk >> 1];
-                const uint32_t w0 = (bk & 1) ? rw.z : rw.x, w1 = (bk & 1) ? rw.w : rw.y;
-                uint32_t h0[4], h1[4];
-                e2m1x8_to_h2x4(w0, h0);
-                e2m1x8_to_h2x4(w1, h1);
+            for (int c = 2 * hh; c < 2 * hh + 2; ++c) {
+                const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) { h0[i] = hmul2(h0[i], s2); h1[i] = hmul2(h1[i], s2); }
-                const int c0 = 2 * bk;  // chunk index among the thread's 16 chunks of 8 channels
-                *reinterpret_cast<uint4*>(Lt + (2 * qq + (c0 >> 3)) * kBlk + sw(key, c0 & 7)) = make_uint4(h0[0], h0[1], h0[2], h0[3]);
-                *reinterpret_cast<uint4*>(Lt + (2 * qq + ((c0 + 1) >> 3)) * kBlk + sw(key, (c0 + 1) & 7)) = make_uint4(h1[0], h1[1], h1[2], h1[3]);
+                for (int i = 0; i < 4; ++i) {  // 8 channels; two code words share a scale
+                    const uint32_t s2 = scale_h2((rsc[c >> 1] >> (16 * (c & 1) + 8 * (i >> 1))) & 0xFFu);
+                    uint32_t h[4];
+                    e2m1x8_to_h2x4(w[i], h);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) h[k] = hmul2(h[k], s2);
+                    *reinterpret_cast<uint4*>(Lt + (2 * c + (qq >> 1)) * kBlk + sw(lkey, 4 * (qq & 1) + i)) =
+                        make_uint4(h[0], h[1], h[2], h[3]);
+                }
             }
         } else {
-            // window row: channels 128 qq .. +63 from the registers, then the other 64 channels
-            // (loaded here, once per row, to keep register pressure below the limit)
+            if (hh == 1) {
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                if (hh == 1) {
+                for (int c = 0; c < 4; ++c) raw[c] = more ? __ldg(win_src() + 16 + 4 * c) : make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) raw[c] = kvalid_dq ? __ldg(win_src() + 4 + c) : make_uint4(0, 0, 0, 0);
-                }
+            for (int c = 0; c < 4; ++c) {  // 16 window channels: two chunks of 64-channel block 4 hh + c
+                const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {  // 8 window channels per chunk
-                    const uint4 rw = raw[c >> 1];
-                    const uint32_t w0 = (c & 1) ? rw.z : rw.x, w1 = (c & 1) ? rw.w : rw.y;
-                    const uint4 h = make_uint4(e4m3x2_to_h2((uint16_t)(w0 & 0xFFFFu)), e4m3x2_to_h2((uint16_t)(w0 >> 16)),
-                                               e4m3x2_to_h2((uint16_t)(w1 & 0xFFFFu)), e4m3x2_to_h2((uint16_t)(w1 >> 16)));
-                    *reinterpret_cast<uint4*>(Lt + (2 * qq + hh) * kBlk + sw(key, c)) = h;
-                }
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<uint4*>(Lt + (4 * hh + c) * kBlk + sw(lkey, 2 * qq + i)) =
+                        make_uint4(e4m3x2_to_h2((uint16_t)(w[2 * i] & 0xFFFFu)), e4m3x2_to_h2((uint16_t)(w[2 * i] >> 16)),
+                                   e4m3x2_to_h2((uint16_t)(w[2 * i + 1] & 0xFFFFu)), e4m3x2_to_h2((uint16_t)(w[2 * i + 1] >> 16)));
             }
         }
     };
@@ -292,14 +291,14 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     __syncthreads();  // barriers, s_m, indices
     load_tile(0);
     {   // Q -> fp16 (B operand of S^T, K-major: row = head, 64-channel blocks)
-        const int h = tid >> 3, cb = tid & 7;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
+            const int g = tid + kT * c, h = g >> 6, ch = g & 63;  // head, 8-channel chunk
             const uint32_t w[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
             uint32_t hv[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) hv[i] = pack_h2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-            *reinterpret_cast<uint4*>(Qs + cb * kQBlk + sw(h, c)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+            *reinterpret_cast<uint4*>(Qs + (ch >> 3) * kQBlk + sw(h, ch & 7)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
         }
     }
     fence_async_smem();
@@ -313,38 +312,34 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
 #pragma unroll
     for (int i = 0; i < 16; ++i) lsum[i] = 0.f;
 
-    // Per tile j: each channel half of L is dequantised by its 256 threads as soon as the O^T MMAs
-    // of tile j - 1 that read that half have completed (O^T m-tiles 0, 1 read half 0, m-tiles 2, 3
-    // half 1), and the S^T k-steps of a half are issued as soon as the half is in shared memory, so
-    // that dequantisation overlaps the tensor pipe. The softmax then runs on all 16 warps.
+    // Per tile j: each channel half of L is dequantised as soon as the O^T MMAs of tile j - 1 that read it
+    // have completed (O^T m-tiles 0, 1 read half 0, m-tiles 2, 3 half 1), and the S^T k-steps of a half are
+    // issued as soon as the half is in shared memory, so that dequantisation overlaps the tensor pipe.
+    // The softmax then runs on all 16 warps.
     for (int j = 0; j < nt; ++j) {
         const bool fp4 = t0 + j < ft;  // CTA-uniform
-        const bool valid = kvalid;
-        if (j > 0) wait_bar(half ? kBarO1 : kBarO0, (uint32_t)(j - 1) & 1u);
-        dequant(fp4, valid);
-        fence_async_smem();
-        mbar_arrive(&bars[half ? kBarH1 : kBarH0]);
-        if (j + 1 < nt) load_tile(j + 1);  // in flight during this tile's MMAs and softmax
-        if (tid == 0) {
-            wait_bar(kBarH0, (uint32_t)j & 1u);
-            tc_fence_after();
+        const bool more = lkey < nwin;
+        const bool valid = key_valid(j);
 #pragma unroll
-            for (int kk = 0; kk < 16; ++kk) {
-                const uint32_t off = (uint32_t)((kk >> 2) * kBlk + 32 * (kk & 3));
-                const uint32_t qoff = (uint32_t)((kk >> 2) * kQBlk + 32 * (kk & 3));
-                mma_f16(tb + kSCol, sw128_desc(smem_u32(Lt) + off), sw128_desc(smem_u32(Qs) + qoff), kIdescS, kk > 0);
-            }
-            wait_bar(kBarH1, (uint32_t)j & 1u);
-            tc_fence_after();
+        for (int hh = 0; hh < 2; ++hh) {
+            if (j > 0) wait_bar(hh ? kBarO1 : kBarO0, (uint32_t)(j - 1) & 1u);
+            dequant(hh, fp4, more);
+            fence_async_smem();
+            mbar_arrive(&bars[hh ? kBarH1 : kBarH0]);
+            if (hh == 1 && j + 1 < nt) load_tile(j + 1);  // in flight during this tile's MMAs and softmax
+            if (tid == 0) {
+                wait_bar(hh ? kBarH1 : kBarH0, (uint32_t)j & 1u);
+                tc_fence_after();
 #pragma unroll
-            for (int kk = 16; kk < 32; ++kk) {
-                const uint32_t off = (uint32_t)((kk >> 2) * kBlk + 32 * (kk & 3));
-                const uint32_t qoff = (uint32_t)((kk >> 2) * kQBlk + 32 * (kk & 3));
-                mma_f16(tb + kSCol, sw128_desc(smem_u32(Lt) + off), sw128_desc(smem_u32(Qs) + qoff), kIdescS, true);
+                for (int kk = 16 * hh; kk < 16 * hh + 16; ++kk) {
+                    const uint32_t off = (uint32_t)((kk >> 2) * kBlk + 32 * (kk & 3));
+                    const uint32_t qoff = (uint32_t)((kk >> 2) * kQBlk + 32 * (kk & 3));
+                    mma_f16(tb + kSCol, sw128_desc(smem_u32(Lt) + off), sw128_desc(smem_u32(Qs) + qoff), kIdescS, kk > 0);
+                }
+                if (hh == 1) mma_commit(&bars[kBarS]);
             }
-            mma_commit(&bars[kBarS]);
+            __syncwarp();
         }
-        __syncwarp();
         wait_bar(kBarS, (uint32_t)j & 1u);  // also every earlier MMA (the O^T of tile j - 1)
         tc_fence_after();
 
@@ -494,7 +489,7 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if (warp == 0) tmem_dealloc(tb, kCols);
+        if (warp == kT / 32 - 1) tmem_dealloc(tb, kCols);
         return;
     }
     if (tid < 64) {
@@ -527,7 +522,7 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(tb, kCols);
+    if (warp == kT / 32 - 1) tmem_dealloc(tb, kCols);
 }
 
 }  // namespace
