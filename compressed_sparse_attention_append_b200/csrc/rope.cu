@@ -64,9 +64,39 @@ __device__ __forceinline__ Vec<VB> pack(const float* f) {
     return v;
 }
 
+// The cosines and sines of pairs j, j + 1, ..: read at once where there is no norm (whose kernels have no
+// registers to spare for them), one by one where there is.
+template <int N, bool WIDE>
+struct Turns {
+    float c[WIDE ? N : 1], s[WIDE ? N : 1];
+    const float *cp, *sp;
+    __device__ __forceinline__ Turns(const float* cosines, const float* sines) : cp(cosines), sp(sines) {
+        if constexpr (WIDE) {
+            ld(cp, c);
+            ld(sp, s);
+        }
+    }
+    __device__ __forceinline__ float cosine(int i) const { return WIDE ? c[WIDE ? i : 0] : cp[i]; }
+    __device__ __forceinline__ float sine(int i) const { return WIDE ? s[WIDE ? i : 0] : sp[i]; }
+    static __device__ __forceinline__ void ld(const float* p, float (&v)[WIDE ? N : 1]) {
+        if constexpr (N % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(p + i);
+                v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+            }
+        } else if constexpr (N == 2) {
+            const float2 f = *reinterpret_cast<const float2*>(p);
+            v[0] = f.x, v[1] = f.y;
+        } else {
+            v[0] = *p;
+        }
+    }
+};
+
 // One row per group of a.lanes lanes, CPL vectors per lane; ITER rows of a group are in flight, and with a
 // norm a group takes a.rounds * ITER rows in turn. Measured for 4096 tokens x 64 heads x 512, bf16: the
-// rotation alone is fastest with two rows in flight and one round (83 us, 6.4 TB/s); the norm, whose
+// rotation alone is fastest with four rows in flight and one round (83 us, 6.4 TB/s; two rows 88); the norm, whose
 // instructions weigh as much as its bytes, with one row, eight rounds and five blocks an SM (99 us,
 // 5.5 TB/s; one round 108, two rows 118). Rows of 128 channels: 16384 tokens x 33 heads 81 us (3.4 TB/s), in
 // halves over the whole head 16384 x 20 heads 46 us (3.7 TB/s): shorter rows, more instructions per byte.
@@ -74,7 +104,7 @@ template <typename T, int VB, int CPL, int ITER, bool NORM, bool HALF>
 __global__ void __launch_bounds__(kThr, NORM && CPL <= 2 ? (HALF ? 4 : 5) : 1) rotate_kernel(RotateArgs a) {
     constexpr int E = VB / (int)sizeof(T);
     using V = Vec<VB>;
-    extern __shared__ float table[];  // [tokens of the block][rot / 2] cosines, then the sines
+    extern __shared__ __align__(16) float table[];  // [tokens of the block][rot / 2] cosines, then the sines
     // where a row is always a warp's, its number, and all that follows from it, is the same in every lane
     constexpr bool WARP = CPL > (HALF ? 2 : 1);
     const int tid = threadIdx.x, lanes = WARP ? 32 : a.lanes, per = kThr / lanes;
@@ -194,18 +224,19 @@ __global__ void __launch_bounds__(kThr, NORM && CPL <= 2 ? (HALF ? 4 : 5) : 1) r
                     if (turned[c]) {
                         if constexpr (HALF) {
                             const int j = at[c] - a.offset;
+                            const Turns<E, !NORM> t(cosines + j, sn + j);
 #pragma unroll
                             for (int e = 0; e < E; ++e) {
-                                const float cv = cosines[j + e], sv = sn[j + e];
-                                const float y0 = fmaf(f[0][e], cv, -f[1][e] * sv);
+                                const float cv = t.cosine(e), sv = t.sine(e), y0 = fmaf(f[0][e], cv, -f[1][e] * sv);
                                 f[1][e] = fmaf(f[1][e], cv, f[0][e] * sv);
                                 f[0][e] = y0;
                             }
                         } else {
                             const int j = (at[c] - a.offset) >> 1;
+                            const Turns<E / 2, !NORM> t(cosines + j, sn + j);
 #pragma unroll
                             for (int e = 0; e < E; e += 2) {
-                                const float cv = cosines[j + e / 2], sv = sn[j + e / 2];
+                                const float cv = t.cosine(e / 2), sv = t.sine(e / 2);
                                 const float y0 = fmaf(f[0][e], cv, -f[0][e + 1] * sv);
                                 f[0][e + 1] = fmaf(f[0][e + 1], cv, f[0][e] * sv);
                                 f[0][e] = y0;
@@ -285,8 +316,8 @@ cudaError_t launch_vec(RotateArgs a, cudaStream_t s) {
     };
     // Rounds: the index arithmetic, the table and the weights are once per block, so with a norm a block takes
     // up to eight rounds of rows while six blocks an SM remain and the table stays small. (One round's table
-    // is at most 33 KB: rows * rot / 2 <= 256 / lanes * ITER * lanes * CPL * E / 2 pairs with
-    // ITER * CPL * E <= 32, and one token more of up to 512 pairs.)
+    // is at most 36 KB: rows * rot / 2 <= 256 / lanes * ITER * lanes * CPL * E / 2 pairs with
+    // ITER * CPL * E <= 32 but for the case of four rows, and one token more of up to 512 pairs.)
     a.rounds = 1;
     while (NORM && a.rounds < 8 && all >= (int64_t)148 * 6 * rows * a.rounds * 2 && table((int64_t)rows * a.rounds * 2) <= 16384)
         a.rounds *= 2;
@@ -308,9 +339,14 @@ cudaError_t launch_rows(RotateArgs a, cudaStream_t s) {
     const bool many = a.tokens * a.heads >= (int64_t)148 * 8 * (kThr / a.lanes) * 2;
     if (need <= 32)
         return many ? launch_vec<T, VB, G, NORM ? 1 : 4 / G, NORM, HALF>(a, s) : launch_vec<T, VB, G, 1, NORM, HALF>(a, s);
-    if (need <= 64)
-        return many ? launch_vec<T, VB, 2 * G, NORM || HALF ? 1 : 2, NORM, HALF>(a, s)
-                    : launch_vec<T, VB, 2 * G, 1, NORM, HALF>(a, s);
+    if (need <= 64) {
+        if constexpr (!NORM && !HALF) {
+            // four rows in flight where the table of 32 rows is small (few heads rotated whole: 64 KB)
+            if (many && (31 / a.heads + 2) * (a.rot / 2) * (int)sizeof(float2) <= 32768)
+                return launch_vec<T, VB, 2, 4, NORM, HALF>(a, s);
+        }
+        return launch_vec<T, VB, 2 * G, 1, NORM, HALF>(a, s);
+    }
     if (need <= 128) return launch_vec<T, VB, 4 * G, 1, NORM, HALF>(a, s);
     if constexpr (!HALF) return launch_vec<T, VB, 8, 1, NORM, HALF>(a, s);  // (256 vectors at most)
     return cudaErrorInvalidValue;

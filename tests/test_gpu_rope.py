@@ -48,6 +48,8 @@ CASES = [  # tokens, heads, d, rot, offset
     (9, 3, 7, 6, 1),         # odd width and offset
     (4, 2, 130, 2, 127), (2, 2, 1, 0, 0), (6, 4, 96, 0, 0),
     (2500, 16, 64, 64, 0),   # several rows per group of lanes
+    (20000, 1, 512, 512, 0),  # many tokens of one head, rotated whole: the largest tables
+    (700, 60, 512, 64, 448), (9000, 2, 256, 256, 0),
 ]
 
 
