@@ -259,15 +259,21 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
         if (fp4) {
 #pragma unroll
             for (int c = 2 * hh; c < 2 * hh + 2; ++c) {
-                const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+                // lanes 2 and 3 of a key, which write the next 64-channel block (the same banks), begin with their
+                // second two chunks: the stores of 8 lanes then fall on different banks
+                const bool far = qq >= 2;
+                const uint32_t w[4] = {far ? raw[c].z : raw[c].x, far ? raw[c].w : raw[c].y, far ? raw[c].x : raw[c].z,
+                                       far ? raw[c].y : raw[c].w};
+                const uint32_t s16 = (rsc[c >> 1] >> (16 * (c & 1))) & 0xFFFFu, first = far ? s16 >> 8 : s16 & 0xFFu,
+                               second = far ? s16 & 0xFFu : s16 >> 8;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {  // 8 channels; two code words share a scale
-                    const uint32_t s2 = scale_h2((rsc[c >> 1] >> (16 * (c & 1) + 8 * (i >> 1))) & 0xFFu);
+                    const uint32_t s2 = scale_h2(i < 2 ? first : second);
                     uint32_t h[4];
                     e2m1x8_to_h2x4(w[i], h);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) h[k] = hmul2(h[k], s2);
-                    *reinterpret_cast<uint4*>(Lt + (2 * c + (qq >> 1)) * kBlk + sw(lkey, 4 * (qq & 1) + i)) =
+                    *reinterpret_cast<uint4*>(Lt + (2 * c + (qq >> 1)) * kBlk + sw(lkey, 4 * (qq & 1) + (far ? i ^ 2 : i))) =
                         make_uint4(h[0], h[1], h[2], h[3]);
                 }
             }
