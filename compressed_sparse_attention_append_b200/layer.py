@@ -19,6 +19,7 @@ One decode step of a layer of the pages' own shape, `B` sequences (bf16 unless n
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -61,7 +62,8 @@ def declare(L):
     """The signatures of include/csa2_layer.h on the loaded library."""
     vp, i, i64, u32, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float, ctypes.c_size_t
     dbl, P = ctypes.c_double, ctypes.POINTER
-    R, H, A, C = P(csa2_rope_spec), P(csa2_heads), P(csa2_append_row), P(csa2_paged_cache)
+    # structs travel as their bytes (packing them costs half of filling a ctypes structure)
+    R, H, A, C = P(csa2_rope_spec), vp, vp, P(csa2_paged_cache)
     sig = {
         "csa2_rope_frequencies": [i, dbl, i, dbl, i64, dbl, dbl, vp, P(f)],
         "csa2_rope": [R, i, i64, i, vp, H, vp],
@@ -118,14 +120,42 @@ def _refuse(t, dtype, dev, shape, dense):
     return t.data_ptr()
 
 
-def _ptr(t, dtype, dev, shape=None, dense=True):
-    """A tensor's pointer after the checks that the library cannot make (None stays None)."""
+def _ptr(t, dtype, dev, shape):
+    """The pointer of a dense tensor after the checks that the library cannot make (None stays None)."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and (not dense or t.is_contiguous()) \
-            and (shape is None or t.shape == shape):
-        return t.data_ptr()
-    return _refuse(t, dtype, dev, shape, dense)
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _refuse(t, dtype, dev, shape, True)
+
+
+def _strided(t, dtype, dev, shape):
+    """The same for a tensor whose strides travel with it."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _refuse(t, dtype, dev, shape, False)
+
+
+_heads_bytes = struct.Struct("@PPqqqqPi4x").pack    # csa2_heads
+_row_bytes = struct.Struct("@PqqPP").pack           # csa2_append_row
+assert struct.calcsize("@PPqqqqPi4x") == ctypes.sizeof(csa2_heads)
+assert struct.calcsize("@PqqPP") == ctypes.sizeof(csa2_append_row)
+
+
+_lib = None
+
+
+def _load():
+    """The library, kept here after the first call."""
+    global _lib
+    _lib = lib()
+    return _lib
 
 
 def _status(ws):
@@ -140,9 +170,10 @@ class Rope:
         self.inv_freq, self.offset, self.interleaved = inv_freq, int(offset), bool(interleaved)
         self.mscale, self.inverse = float(mscale), bool(inverse)
         self.rot = 2 * inv_freq.numel()
-        self.c = csa2_rope_spec(_ptr(inv_freq, _F64, _device()), self.rot, self.offset, int(self.interleaved),
+        self.c = csa2_rope_spec(_ptr(inv_freq, _F64, _device(), (self.rot // 2,)), self.rot, self.offset, int(self.interleaved),
                                 int(self.inverse), self.mscale)
         self.ref = ctypes.pointer(self.c)
+        self.at = ctypes.addressof(self.c)
 
     @classmethod
     def for_context(cls, rot, base=10000.0, scaling="plain", factor=1.0, orig_ctx=0, beta_fast=32.0, beta_slow=1.0,
@@ -166,13 +197,14 @@ def csa2_rope_frequencies(rot, base=10000.0, scaling="plain", factor=1.0, orig_c
 
 
 def _heads(x, out, weight, dtype, dev, tokens, d):
-    t, heads, ch = x.shape
+    shape = x.shape
+    t, heads, ch = shape
     x0, x1, x2 = x.stride()
     o0, o1, o2 = out.stride()
     assert t == tokens and ch == d, "expected [tokens, heads, d]"
     assert x2 == 1 and o2 == 1, "expected dense heads (stride 1 along the channels)"
-    return csa2_heads(_ptr(x, dtype, dev, None, False), _ptr(out, dtype, dev, x.shape, False), x0, x1, o0, o1,
-                      None if weight is None else _ptr(weight, dtype, dev, (d,)), heads)
+    return _heads_bytes(_strided(x, dtype, dev, shape), _strided(out, dtype, dev, shape), x0, x1, o0, o1,
+                        0 if weight is None else _ptr(weight, dtype, dev, (d,)), heads)
 
 
 def csa2_rope(rope: Rope, pos, x, out, stream=None):
@@ -181,7 +213,7 @@ def csa2_rope(rope: Rope, pos, x, out, stream=None):
     dtype, dev = x.dtype, _device()
     assert dtype in _TYPES, "expected a bf16 or fp32 tensor"
     h = _heads(x, out, None, dtype, dev, tokens, d)
-    s = lib().csa2_rope(rope.ref, _TYPES[dtype], tokens, d, _ptr(pos, _I64, dev, (tokens,)), ctypes.byref(h),
+    s = (_lib or _load()).csa2_rope(rope.ref, _TYPES[dtype], tokens, d, _ptr(pos, _I64, dev, (tokens,)), h,
                         _stream(stream, dev))
     if s:
         raise Csa2Error("csa2_rope", s)
@@ -194,9 +226,9 @@ def csa2_norm_rope(rope, pos, eps, q, wq, q_out, k=None, wk=None, k_out=None, st
     dtype, dev = q.dtype, _device()
     assert dtype in _TYPES, "expected a bf16 or fp32 tensor"
     hq = _heads(q, q_out, wq, dtype, dev, tokens, d)
-    hk = None if k is None else ctypes.byref(_heads(k, k_out, wk, dtype, dev, tokens, d))
-    s = lib().csa2_norm_rope(None if rope is None else rope.ref, _TYPES[dtype], tokens, d,
-                             _ptr(pos, _I64, dev, (tokens,)), eps, ctypes.byref(hq), hk, _stream(stream, dev))
+    hk = None if k is None else _heads(k, k_out, wk, dtype, dev, tokens, d)
+    s = (_lib or _load()).csa2_norm_rope(None if rope is None else rope.ref, _TYPES[dtype], tokens, d,
+                             _ptr(pos, _I64, dev, (tokens,)), eps, hq, hk, _stream(stream, dev))
     if s:
         raise Csa2Error("csa2_norm_rope", s)
 
@@ -207,7 +239,7 @@ def csa2_fp8_quantize(x, data, scale, stream=None):
     xs, one = x.stride()
     dev = _device()
     assert one == 1 or k == 1, "expected dense rows"
-    s = lib().csa2_fp8_quantize(rows, k, _ptr(x, _BF16, dev, None, False), xs, _ptr(data, _E4M3, dev, (rows, k)),
+    s = (_lib or _load()).csa2_fp8_quantize(rows, k, _strided(x, _BF16, dev, (rows, k)), xs, _ptr(data, _E4M3, dev, (rows, k)),
                                 _ptr(scale, _F32, dev, (-(-k // 128), rows)), _stream(stream, dev))
     if s:
         raise Csa2Error("csa2_fp8_quantize", s)
@@ -218,7 +250,7 @@ def csa2_fp8_quantize_weight(w, data, scale, stream=None):
     n, k = w.shape
     dev = _device()
     _check("csa2_fp8_quantize_weight", lib().csa2_fp8_quantize_weight(
-        n, k, _ptr(w, _BF16, dev), _ptr(data, _E4M3, dev, (n, k)),
+        n, k, _ptr(w, _BF16, dev, (n, k)), _ptr(data, _E4M3, dev, (n, k)),
         _ptr(scale, _F32, dev, (-(-n // 128), -(-k // 128))), _stream(stream, dev)))
 
 
@@ -231,9 +263,9 @@ def csa2_fp8_gemm(x, xs, w, ws, out, status=None, stream=None):
     assert dtype in _TYPES, "expected a bf16 or fp32 tensor"
     assert o1 == 1 or n == 1, "expected dense rows"
     at, size = _status(status)
-    s = lib().csa2_fp8_gemm(m, n, k, _ptr(x, _E4M3, dev), _ptr(xs, _F32, dev, (nb, m)), _ptr(w, _E4M3, dev, (n, k)),
+    s = (_lib or _load()).csa2_fp8_gemm(m, n, k, _ptr(x, _E4M3, dev, (m, k)), _ptr(xs, _F32, dev, (nb, m)), _ptr(w, _E4M3, dev, (n, k)),
                             _ptr(ws, _F32, dev, (-(-n // 128), nb)), _TYPES[dtype],
-                            _ptr(out, dtype, dev, (m, n), False), o0 if o0 > n else n, at, size, _stream(stream, dev))
+                            _strided(out, dtype, dev, (m, n)), o0 if o0 > n else n, at, size, _stream(stream, dev))
     if s:
         raise Csa2Error("csa2_fp8_gemm", s)
 
@@ -281,9 +313,8 @@ def _append_row(x, weight, rope, dev, batch, t, channels):
         return None
     x0, x1, x2 = x.stride()
     assert x2 == 1, f"expected dense rows [{batch}, {t}, {channels}]"
-    return ctypes.byref(csa2_append_row(_ptr(x, _BF16, dev, (batch, t, channels), False), x0, x1,
-                                        None if weight is None else _ptr(weight, _BF16, dev, (channels,)),
-                                        None if rope is None else rope.ref))
+    return _row_bytes(_strided(x, _BF16, dev, (batch, t, channels)), x0, x1,
+                      0 if weight is None else _ptr(weight, _BF16, dev, (channels,)), 0 if rope is None else rope.at)
 
 
 def csa2_paged_append(cache: PagedCache, batch, t, pos, latent=None, idx_k=None, swa=None, rope=None, idx_rope=None,
@@ -295,7 +326,7 @@ def csa2_paged_append(cache: PagedCache, batch, t, pos, latent=None, idx_k=None,
     rpos [B, t] int64: the tokens' positions for the rotation (None: those of the entries)."""
     dev = cache.on(batch)
     at, size = _status(ws)
-    s = lib().csa2_paged_append(
+    s = (_lib or _load()).csa2_paged_append(
         cache.ref, batch, t, _ptr(pos, _I64, dev, (batch,)), _ptr(length, _I32, dev, (batch,)),
         _ptr(rpos, _I64, dev, (batch, t)), eps, _append_row(latent, w_latent, rope, dev, batch, t, 512),
         _append_row(idx_k, w_idx_k, idx_rope, dev, batch, t, 128),
@@ -309,7 +340,7 @@ def csa2_paged_gather(cache: PagedCache, batch, idx, latent=None, key=None, ws=N
     """idx [B, n] int32 entries (-1: zeros) -> latent [B, n, 512] and key [B, n, 128] bf16 (either may be None)."""
     dev, n = cache.on(batch), idx.shape[1]
     at, size = _status(ws)
-    s = lib().csa2_paged_gather(cache.ref, batch, n, _ptr(idx, _I32, dev, (batch, n)),
+    s = (_lib or _load()).csa2_paged_gather(cache.ref, batch, n, _ptr(idx, _I32, dev, (batch, n)),
                                 _ptr(latent, _BF16, dev, (batch, n, 512)), _ptr(key, _BF16, dev, (batch, n, 128)), at,
                                 size, _stream(stream, dev))
     if s:
@@ -321,7 +352,7 @@ def csa2_paged_attend(cache: PagedCache, batch, tq, qpos, q, idx, k, out, swa_be
     """q [B*tq, 64, 512] bf16, idx [B*tq, k] int32 -> out [B*tq, 64, 512] bf16 (tensor cores)."""
     dev, rows = cache.on(batch), batch * tq
     at, size = _status(ws)
-    s = lib().csa2_paged_attend(
+    s = (_lib or _load()).csa2_paged_attend(
         cache.ref, batch, tq, _ptr(qpos, _I64, dev, (rows,)), _ptr(q, _BF16, dev, (rows, 64, 512)),
         _ptr(idx, _I32, dev, (rows, k)), k, _ptr(swa_begin, _I64, dev, (batch,)), win, ratio, sm_scale,
         _ptr(out, _BF16, dev, (rows, 64, 512)), _ptr(out_f32, _F32, dev, (rows, 64, 512)),
@@ -337,7 +368,7 @@ def csa2_paged_index_topk(cache: PagedCache, batch, tq, qpos, idx_q, k, out_idx,
     if max_ctx is None:
         max_ctx = cache.max_pages * cache.page
     at, size = _status(ws)
-    s = lib().csa2_paged_index_topk(
+    s = (_lib or _load()).csa2_paged_index_topk(
         cache.ref, batch, tq, _ptr(qpos, _I64, dev, (rows,)), _ptr(idx_q, _BF16, dev, (rows, hi, 128)), hi, k, ratio,
         max_ctx, flags, _ptr(out_idx, _I32, dev, (rows, k)), at, size, _stream(stream, dev))
     if s:
