@@ -40,10 +40,11 @@ struct PagedAppendArgs {
     double eps;
     AppendRow row[3];        // latent, indexer key, window
     int kinds, kind[3];      // those that are appended
-    int most_rot;            // channels of the widest rotation, rounded up to 4
+    unsigned first[3];       // and the first block of each
+    int warp_bytes;          // shared memory of a warp
     uint32_t* status;
 };
-cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
+cudaError_t launch_paged_append(PagedAppendArgs a, cudaStream_t s);
 
 struct PagedGatherArgs {
     csa2_paged_cache c;

@@ -230,11 +230,7 @@ csa2_status csa2_paged_append(const csa2_paged_cache* cache, int batch, int t, c
     a.eps = (double)eps;
     a.status = reinterpret_cast<uint32_t*>(ws);
     for (int i = 0; i < 3; ++i)
-        if (a.row[i].x) {
-            a.kind[a.kinds++] = i;
-            const int rot = a.row[i].inv_freq ? (a.row[i].rot + 3) / 4 * 4 : 0;
-            if (rot > a.most_rot) a.most_rot = rot;
-        }
+        if (a.row[i].x) a.kind[a.kinds++] = i;
     return from_cuda(launch_paged_append(a, (cudaStream_t)stream));
 }
 

@@ -16,9 +16,10 @@
 // and sine are off by 2^-21.4. So e = 2^-21 |y|, and 2^-20 m (|a| + |b|) for the channels of a rotated pair
 // (a, b), cover y and its quotient.
 //
-// Work split: one warp per row (a token's latent, indexer key or window row), 16 channels per lane
-// (one scale block of the latent) or 4 (an eighth of an MXFP4 block). A row's rotated pairs are turned
-// by as many lanes, one pair each, through shared memory.
+// Work split: 16 channels per lane (one scale block of the latent, half an MXFP4 block), so a warp takes one
+// latent or window row, or the indexer keys of four tokens. A row's rotated pairs are turned by its
+// lanes in turn, through shared memory. A row is a chain of loads and some 500 instructions, which bound it
+// (issue slots 76 % busy): 16 sequences of 2048 tokens at most, 853 on average, take 27 us.
 #include "csa2_internal.cuh"
 #include "csa2_layer.cuh"
 
@@ -191,12 +192,16 @@ constexpr float kErr = 1.f / 2097152.f, kErrTurn = 1.f / 1048576.f;  // 2^-21, 2
 
 // y, and L: a value y[i] is within |y[i]| kErr + L of the row's (L: the largest bound of this lane's rotated
 // channels). False where fp32 cannot hold the row's norm (squares past its range): no bound is valid then.
-template <int N>
-__device__ __forceinline__ bool quick_row(const AppendRow& R, const uint16_t* src, int64_t rpos, float eps,
-                                          const WarpMem& sm, int lane, float (&y)[N], float& L) {
+// The row lies on LANES lanes, `lane` of them this one; a row that is not live is read as zeros.
+template <int LANES>
+__device__ __forceinline__ bool quick_row(const AppendRow& R, bool live, const uint16_t* src, int64_t rpos, float eps,
+                                          const WarpMem& sm, int lane, float (&y)[16], float& L) {
+    constexpr int N = 16;
     float w[N];
-    load_row<N>(src, lane, y);
-    load_row<N>(R.weight, lane, w);
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = 0.f;
+    if (live) load16_bf16(src + lane * N, y);
+    load16_bf16(R.weight + lane * N, w);
     // sine and cosine of this lane's first pair are formed while the row is on its way
     const int half = R.inv_freq ? R.rot >> 1 : 0;
     float c0 = 0.f, s0 = 0.f;
@@ -211,9 +216,9 @@ __device__ __forceinline__ bool quick_row(const AppendRow& R, const uint16_t* sr
         for (int i = 0; i < o; ++i) t[i] += t[i + o];
     double ss = (double)t[0];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     // 1 / sqrt with one step of Newton's iteration, the product's rounding carried along
-    const float mean = (float)fma(ss, 1.0 / (32 * N), (double)eps), r0 = rsqrtf(mean), h = mean * r0;
+    const float mean = (float)fma(ss, 1.0 / (LANES * N), (double)eps), r0 = rsqrtf(mean), h = mean * r0;
     const float r = fmaf(0.5f * r0, fmaf(-h, r0, 1.f) - fmaf(mean, r0, -h) * r0, r0);
 #pragma unroll
     for (int i = 0; i < N; ++i) y[i] = (y[i] * w[i]) * r;  // (two bf16 factors: exact)
@@ -236,7 +241,7 @@ __device__ __forceinline__ bool quick_row(const AppendRow& R, const uint16_t* sr
         }
         __syncwarp();
         const float m = (float)R.mscale, me = fabsf(m) * kErrTurn;
-        for (int j = lane; j < half; j += 32) {
+        for (int j = lane; j < half; j += LANES) {
             if (j != lane) sincospif((float)half_turns(rpos, R.inv_freq[j]), &s0, &c0);
             const int2 p = pair_of(R, j);
             const float a = ys[p.x], b = ys[p.y], err = (fabsf(a) + fabsf(b)) * me;
@@ -293,35 +298,36 @@ __device__ __forceinline__ bool quick_latent(const float (&y)[16], float L, Code
     return __all_sync(0xffffffffu, c.scale == (sc >> 8) && (none || (lo[0] == hi[0] && lo[1] == hi[1])));
 }
 
-__device__ __forceinline__ bool quick_key(const float (&y)[4], float L, Coded& c) {
-    float top = 0.f, most = L;
+// half an MXFP4 block; certain of this lane's channels alone
+__device__ __forceinline__ bool quick_key(const float (&y)[16], float L, Coded& c) {
+    float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(y[i]));
-#pragma unroll
-    for (int o = 4; o; o >>= 1) {  // the block's 8 lanes
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    }
-    const float err = fmaf(top, kErr, most), hi = top + err;
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(y[i]));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));  // the block's other lane
+    const float most = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, 1)), err = fmaf(top, kErr, most), hi = top + err;
     // the exponents of both ends: all zeros, or far above the smallest normal number (w / sqrt(mean) is then
     // normal wherever it matters)
     const int xl = (int)(__float_as_uint(fmaxf(top - err, 0.f)) >> 23), xh = (int)(__float_as_uint(hi) >> 23);
-    const bool sure = hi == 0.f || (xl == xh && xl > 64 && xl < 255);
-    c.scale = hi == 0.f ? 0u : (uint32_t)(xl - 2);
-    const float inv = hi == 0.f ? 0.f : __uint_as_float((uint32_t)(254 - (xl - 2)) << 23);  // 2^(127 - scale)
+    const bool none = hi == 0.f;
+    c.scale = none ? 0u : (uint32_t)(xl - 2);
+    const float inv = none ? 0.f : __uint_as_float((uint32_t)(254 - (xl - 2)) << 23);  // 2^(127 - scale)
     const float d = L * inv;
-    uint32_t l = 0u, h = 0u;
-    if (hi != 0.f) {
+    uint32_t lo[2], up[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float a = y[2 * j] * inv, b = y[2 * j + 1] * inv;
-            const float da = fmaf(fabsf(a), kErr, d), db = fmaf(fabsf(b), kErr, d);
-            l |= f32x2_to_e2m1x2(a - da, b - db) << (8 * j);
-            h |= f32x2_to_e2m1x2(a + da, b + db) << (8 * j);
+    for (int h = 0; h < 2; ++h) {
+        float l[8], u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float a = y[8 * h + j] * inv, da = fmaf(fabsf(a), kErr, d);
+            l[j] = a - da;
+            u[j] = a + da;
         }
+        lo[h] = e2m1x8(l);
+        up[h] = e2m1x8(u);
     }
-    c.codes.x = l;
-    return __all_sync(0xffffffffu, sure && l == h);
+    c.codes.x = none ? 0u : lo[0];
+    c.codes.y = none ? 0u : lo[1];
+    return none || (xl == xh && xl > 64 && xl < 255 && lo[0] == up[0] && lo[1] == up[1]);
 }
 
 __device__ __forceinline__ bool quick_window(const float (&y)[16], float L, Coded& c) {
@@ -336,72 +342,102 @@ __device__ __forceinline__ bool quick_window(const float (&y)[16], float L, Code
     return __all_sync(0xffffffffu, lo[0] == hi[0] && lo[1] == hi[1] && lo[2] == hi[2] && lo[3] == hi[3]);
 }
 
+// Where token `tok` of one kind of row is read and written.
+struct Token {
+    bool live;            // to be written
+    const uint16_t* src;
+    int64_t rpos;         // its position for the rotation
+    int64_t row;          // plane row (latent, key) or ring row (window)
+};
+// `first`: one lane of those that work on the token, which reports what is wrong with it
+__device__ __forceinline__ Token locate(const PagedAppendArgs& a, int kind, int64_t tok, int64_t tokens, bool first) {
+    Token k{};
+    if (tok >= tokens) return k;
+    // (in 32 bits where they suffice: a 64-bit division costs a fifth of a row's arithmetic)
+    const int b = tokens <= 0x7FFFFFFF ? (int)((uint32_t)tok / (uint32_t)a.t) : (int)(tok / a.t);
+    const int i = (int)(tok - (int64_t)b * a.t);
+    const int64_t p0 = a.pos[b], p = p0 + i;
+    const int n = a.len ? a.len[b] : a.t;
+    const int64_t cap = a.pg.max_pages << a.pg.shift;
+    if (n < 0 || n > a.t || (n > 0 && (p0 < 0 || (kind < 2 && (p0 > cap || p0 + n > cap))))) {
+        if (i == 0 && first) set_status(a.status, CSA2_DEV_BAD_POS);
+        return k;
+    }
+    if (i >= n) return k;  // padding
+    if (kind == 2) {
+        // the ring keeps the latest swa_cap tokens: an older one of this call shares its slot with a newer one
+        if ((int64_t)i < (int64_t)n - a.c.swa_cap) return k;
+        const int64_t slot = paged_slot(a.pg, b);
+        k.live = slot >= 0;
+        k.row = slot * a.c.swa_cap + (p & (a.c.swa_cap - 1));
+    } else {
+        k.row = paged_row(a.pg, b, p);
+        k.live = k.row >= 0;
+    }
+    if (!k.live && first) set_status(a.status, CSA2_DEV_BAD_PAGE);
+    const AppendRow& R = a.row[kind];
+    k.src = R.x + (int64_t)b * R.x_batch + (int64_t)i * R.x_token;
+    k.rpos = a.rpos ? a.rpos[tok] : p;
+    return k;
+}
+
 // (the arguments stay in constant memory: the 64-bit functions take references into them)
 __global__ void __launch_bounds__(32 * kWarps, kBlocks) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-    const WarpMem sm{smem + 8 * (size_t)a.most_rot * warp, a.most_rot};
     wait_prior_grid();  // the rows come from, and the slots may still be read by, earlier work
-    const int64_t tok = (int64_t)blockIdx.x * kWarps + warp, tokens = (int64_t)a.batch * a.t;
-    if (tok >= tokens) return;
-    const int kind = a.kind[blockIdx.y];
-    // (in 32 bits where they suffice: a 64-bit division costs a fifth of a row's arithmetic)
-    const int b = tokens <= 0x7FFFFFFF ? (int)((uint32_t)tok / (uint32_t)a.t) : (int)(tok / a.t);
-    const int i = (int)(tok - (int64_t)b * a.t);
+    // a kind's rows lie together (their work is alike): blocks first[i] .. first[i + 1] - 1 are kind[i]'s
+    int at = 0;
+    while (at + 1 < a.kinds && blockIdx.x >= a.first[at + 1]) ++at;
+    const int kind = a.kind[at];
     const AppendRow& R = a.row[kind];
-    const int64_t p0 = a.pos[b], p = p0 + i;
-    const int n = a.len ? a.len[b] : a.t;
-    const bool tell = i == 0 && lane == 0;
-    const int64_t cap = a.pg.max_pages << a.pg.shift;
-    if (n < 0 || n > a.t || (n > 0 && (p0 < 0 || (kind < 2 && (p0 > cap || p0 + n > cap))))) {
-        if (tell) set_status(a.status, CSA2_DEV_BAD_POS);
-        return;
-    }
-    if (i >= n) return;  // padding
-    const uint16_t* src = R.x + (int64_t)b * R.x_batch + (int64_t)i * R.x_token;
-    const int64_t rpos = a.rpos ? a.rpos[tok] : p;
+    const int64_t wid = (int64_t)(blockIdx.x - a.first[at]) * kWarps + warp, tokens = (int64_t)a.batch * a.t;
+    unsigned char* const mem = smem + (size_t)a.warp_bytes * warp;
+    const WarpMem sm{mem, a.warp_bytes / 8};
     const float eps = (float)a.eps;
     Coded c{};
-    if (kind == 2) {
-        // the ring keeps the latest swa_cap tokens: an older one of this call shares its slot with a newer one
-        if ((int64_t)i < (int64_t)n - a.c.swa_cap) return;
-        const int64_t slot = paged_slot(a.pg, b);
-        if (slot < 0) {
-            if (lane == 0) set_status(a.status, CSA2_DEV_BAD_PAGE);
-            return;
-        }
+    float y[16], L;
+    if (kind == 1) {
+        // the keys of four tokens, 8 lanes each
+        const int g = lane >> 3, gl = lane & 7, rot = (R.rot + 3) & ~3;
+        const Token k = locate(a, 1, wid * 4 + g, tokens, gl == 0);
+        if (!__any_sync(0xffffffffu, k.live)) return;
         bool sure = false;
         if (R.weight) {
-            float y[16], L;
-            sure = quick_row<16>(R, src, rpos, eps, sm, lane, y, L) && quick_window(y, L, c);
+            const bool held = quick_row<8>(R, k.live, k.src, k.rpos, eps, WarpMem{mem + 8 * rot * g, rot}, gl, y, L);
+            sure = quick_key(y, L, c) && held;
         }
-        if (!sure) c = exact_window(R, src, rpos, a.eps, sm, lane);
-        uint8_t* dst = a.c.swa + (slot * a.c.swa_cap + (p & (a.c.swa_cap - 1))) * kLatSwa + lane * 16;
-        *reinterpret_cast<uint4*>(dst) = c.codes;
+        sure = ((__ballot_sync(0xffffffffu, sure) >> (8 * g)) & 0xFFu) == 0xFFu;
+        if (k.live && sure) {
+            *reinterpret_cast<uint2*>(a.c.k_data + k.row * kLatKBytes + gl * 8) = make_uint2(c.codes.x, c.codes.y);
+            if (!(gl & 1)) a.c.k_scale[k.row * kLatKScales + (gl >> 1)] = (uint8_t)c.scale;
+        }
+        unsigned todo = __ballot_sync(0xffffffffu, gl == 0 && k.live && !sure);
+        for (; todo; todo &= todo - 1) {  // the others by the whole warp, one after the other
+            const int from = __ffs(todo) - 1;
+            const int64_t row = __shfl_sync(0xffffffffu, k.row, from), rpos = __shfl_sync(0xffffffffu, k.rpos, from);
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(
+                __shfl_sync(0xffffffffu, (unsigned long long)(uintptr_t)k.src, from));
+            c = exact_key(R, src, rpos, a.eps, sm, lane);
+            *reinterpret_cast<uint16_t*>(a.c.k_data + row * kLatKBytes + lane * 2) = (uint16_t)c.codes.x;
+            if (!(lane & 7)) a.c.k_scale[row * kLatKScales + (lane >> 3)] = (uint8_t)c.scale;
+        }
         return;
     }
-    const int64_t row = paged_row(a.pg, b, p);
-    if (row < 0) {
-        if (lane == 0) set_status(a.status, CSA2_DEV_BAD_PAGE);
-        return;
-    }
+    const Token k = locate(a, kind, wid, tokens, lane == 0);
+    if (!k.live) return;
     bool sure = false;
+    if (R.weight) {
+        sure = quick_row<32>(R, true, k.src, k.rpos, eps, sm, lane, y, L);
+        sure = (kind == 0 ? quick_latent(y, L, c) : quick_window(y, L, c)) && sure;
+    }
     if (kind == 0) {
-        if (R.weight) {
-            float y[16], L;
-            sure = quick_row<16>(R, src, rpos, eps, sm, lane, y, L) && quick_latent(y, L, c);
-        }
-        if (!sure) c = exact_latent(R, src, rpos, a.eps, sm, lane);
-        *reinterpret_cast<uint2*>(a.c.l_data + row * kLatBytes + lane * 8) = make_uint2(c.codes.x, c.codes.y);
-        a.c.l_scale[row * kLatScales + lane] = (uint8_t)c.scale;
+        if (!sure) c = exact_latent(R, k.src, k.rpos, a.eps, sm, lane);
+        *reinterpret_cast<uint2*>(a.c.l_data + k.row * kLatBytes + lane * 8) = make_uint2(c.codes.x, c.codes.y);
+        a.c.l_scale[k.row * kLatScales + lane] = (uint8_t)c.scale;
     } else {
-        if (R.weight) {
-            float y[4], L;
-            sure = quick_row<4>(R, src, rpos, eps, sm, lane, y, L) && quick_key(y, L, c);
-        }
-        if (!sure) c = exact_key(R, src, rpos, a.eps, sm, lane);
-        *reinterpret_cast<uint16_t*>(a.c.k_data + row * kLatKBytes + lane * 2) = (uint16_t)c.codes.x;
-        if (!(lane & 7)) a.c.k_scale[row * kLatKScales + (lane >> 3)] = (uint8_t)c.scale;
+        if (!sure) c = exact_window(R, k.src, k.rpos, a.eps, sm, lane);
+        *reinterpret_cast<uint4*>(a.c.swa + k.row * kLatSwa + lane * 16) = c.codes;
     }
 }
 
@@ -460,12 +496,21 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(PagedGatherArgs a) {
 
 }  // namespace
 
-cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
-    const int64_t grid = ((int64_t)a.batch * a.t + kWarps - 1) / kWarps;
-    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    // a kind's rows lie together: their work is alike
-    return launch_after_prior(paged_append_kernel, dim3((unsigned)grid, (unsigned)a.kinds), dim3(32 * kWarps),
-                              (size_t)8 * a.most_rot * kWarps, s, a);
+cudaError_t launch_paged_append(PagedAppendArgs a, cudaStream_t s) {
+    const int64_t tokens = (int64_t)a.batch * a.t;
+    int64_t blocks = 0;
+    for (int i = 0; i < a.kinds; ++i) {
+        const int per = kWarps * (a.kind[i] == 1 ? 4 : 1);  // tokens of a block
+        a.first[i] = (unsigned)blocks;
+        blocks += (tokens + per - 1) / per;
+        if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+        // 8 bytes per rotated channel of the rows that a warp holds
+        const int rot = a.row[a.kind[i]].inv_freq ? (a.row[a.kind[i]].rot + 3) / 4 * 4 : 0;
+        const int bytes = 8 * rot * (a.kind[i] == 1 ? 4 : 1);
+        if (bytes > a.warp_bytes) a.warp_bytes = bytes;
+    }
+    return launch_after_prior(paged_append_kernel, dim3((unsigned)blocks), dim3(32 * kWarps), (size_t)a.warp_bytes * kWarps,
+                              s, a);
 }
 
 cudaError_t launch_paged_gather(const PagedGatherArgs& a, cudaStream_t s) {
