@@ -42,7 +42,8 @@ __device__ __forceinline__ void set_status(uint32_t* status, uint32_t bit) {
 
 // ---- codec helpers -----------------------------------------------------------------------------
 // Two E2M1 codes (one byte: low nibble = first element) -> half2 (low half = first element).
-// Hardware conversion cvt.rn.f16x2.e2m1x2 (sm_100a); exact, every E2M1 value is an fp16 value.
+// Hardware conversion cvt.rn.f16x2.e2m1x2 (sm_100a); exact, every E2M1 value is an fp16 value. w has to be a
+// whole 32-bit load: with its upper half known to be zero the compiler has given zeros for the lower.
 __device__ __forceinline__ void e2m1x8_to_h2x4(uint32_t w, uint32_t (&h)[4]) {
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
         "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
