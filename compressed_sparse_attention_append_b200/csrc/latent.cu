@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     const int b = row / a.tq;
     const int64_t qpos = a.qpos[row];
     const int64_t qlast = qpos < 0 ? -1 : (qpos + 1) / a.ratio - 1;  // the last visible entry
-    const bool row_ok = qpos >= 0 && qlast < a.c.cap;
+    // (a page table bounds its own entries, each index is checked against it: the window needs none of them)
+    const bool row_ok = qpos >= 0 && (PAGED || qlast < a.c.cap);
     int64_t lo = qpos - a.win + 1;
     {
         const int64_t sb = a.swa_begin ? a.swa_begin[b] : 0;

@@ -105,7 +105,7 @@ CSA2_API csa2_status csa2_rope(const csa2_rope_spec* rope, int dtype, int64_t to
  * Norm of each head and its rotation in one pass, queries and keys in one launch:
  *   out = R_pos(x * w / sqrt(mean(x^2) + eps))   for the heads of q and of k (k may be NULL)
  * rope may be NULL (the norm alone; pos may then be NULL too). No rounding between norm and rotation;
- * otherwise as csa2_rope. eps >= 0.
+ * the sum of squares is fp32 (rows beyond about 1e19 overflow it); otherwise as csa2_rope. eps >= 0.
  */
 CSA2_API csa2_status csa2_norm_rope(const csa2_rope_spec* rope, int dtype, int64_t tokens, int d, const int64_t* pos,
                                     float eps, const csa2_heads* q, const csa2_heads* k, void* stream);
@@ -196,8 +196,8 @@ typedef struct {
  * A sequence whose entries leave [0, max_pages * page), or with len outside [0, t], sets
  * CSA2_DEV_BAD_POS and is skipped (window rows need pos >= 0 alone); a token whose page is not there
  * sets CSA2_DEV_BAD_PAGE and is skipped. ws: at least 256 bytes from csa2_workspace_init for these
- * bits, or NULL. Two tokens that share a slot (sequences with a common page, say) leave it undefined
- * which one it holds.
+ * bits, or NULL. Two tokens of a call that share a slot (sequences with a common page, say) leave its
+ * contents undefined.
  */
 CSA2_API csa2_status csa2_paged_append(const csa2_paged_cache* cache, int batch, int t, const int64_t* pos,
                                        const int32_t* len, const int64_t* rpos, float eps,

@@ -341,6 +341,45 @@ def test_attend_rows_without_keys_bad_entries_and_missing_pages():
     _close(out[2], of[2], lse[2], *_reference(c, 2, qpos[2], q[2], idx[2], 128, 1, 0, 512 ** -0.5))
 
 
+def test_the_window_alone_and_tokens_past_the_table():
+    """k = 0 needs no page: the window counts wherever the token is. Entries past the table are refused one by one."""
+    c, _ = _filled(1, 300, 8, 512, seed=9)
+    few = csa.PagedCache(c.n_pages, 8, 1, 2, 512, n_slots=c.n_slots, swa_slot=c.swa_slot, page_table=c.table[:, :2].contiguous(),
+                         l_data=c.l_data, l_scale=c.l_scale, k_data=c.k_data, k_scale=c.k_scale, swa=c.swa)
+    none = csa.PagedCache(0, 8, 1, 0, 512, n_slots=c.n_slots, swa_slot=c.swa_slot, swa=c.swa, latent=False, indexer=False,
+                          page_table=torch.empty(1, 0, dtype=torch.int32, device=DEV))
+    q, qp = _rand(3, 1, 64, 512), torch.tensor([299], device=DEV)
+    want = _reference(c, 0, 299, q[0], [], 128, 1, 0, 512 ** -0.5)
+    for cache in (c, few, none):
+        out, of, lse, st = _attend(csa.csa2_paged_attend, cache, 1, 1, qp, q, None, 0)
+        assert st == 0
+        _close(out[0], of[0], lse[0], *want)
+    idx = torch.tensor([[3, 15, 16, 3]], dtype=torch.int32, device=DEV)  # (an entry twice counts twice)
+    out, of, lse, st = _attend(csa.csa2_paged_attend, few, 1, 1, qp, q, idx, 4)
+    assert st == csa.CSA2_DEV_BAD_INDEX
+    _close(out[0], of[0], lse[0], *_reference(few, 0, 299, q[0], idx[0], 128, 1, 0, 512 ** -0.5))
+
+
+def test_pages_shared_by_sequences_and_two_calls_at_once():
+    """Sequences with a common prefix read the same pages; calls on two streams share nothing but the cache."""
+    c, _ = _filled(3, 256, 16, 128, seed=11)
+    c.table[1, :8] = c.table[0, :8]
+    c.table[2, :16] = c.table[0, :16]
+    q, qp = _rand(4, 3, 64, 512), torch.tensor([255, 200, 255], device=DEV)
+    idx = _select(3, [256, 201, 256], 100, seed=5)
+    out, of, lse, st = _attend(csa.csa2_paged_attend, c, 3, 1, qp, q, idx, 100)
+    assert st == 0
+    for r in range(3):
+        _close(out[r], of[r], lse[r], *_reference(c, r, int(qp[r]), q[r], idx[r], 128, 1, 0, 512 ** -0.5))
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], [torch.empty_like(out) for _ in range(2)]
+    for _ in range(10):
+        for s, o in zip(streams, outs):
+            csa.csa2_paged_attend(c, 3, 1, qp, q, idx, 100, o, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], out) and torch.equal(outs[1], out)
+
+
 @pytest.mark.parametrize("B,tq,n,hi,k,page,flags", [(2, 1, 700, 32, 64, 16, 1), (1, 3, 2500, 4, 512, 64, 0), (3, 1, 20, 8, 64, 8, 1)])
 def test_index_over_pages_is_the_contiguous_selection(B, tq, n, hi, k, page, flags):
     c, flat = _filled(B, n, page, 128, seed=n + hi)
