@@ -173,6 +173,10 @@ __device__ __forceinline__ int sub_bin(unsigned long long key) {
 // first access to data an earlier kernel wrote (a no-op when launched without the attribute).
 __device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets the next kernel on the stream start beside this one once every CTA of this grid has come here; its
+// own wait_prior_grid still waits for this grid's end, so only what it does before that overlaps.
+__device__ __forceinline__ void start_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_after_prior(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                                       Args... args) {

@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(int64_t rows, int k, cons
                                                        uint8_t* data, float* scale) {
     const int l = threadIdx.x & 15, nb = (k + 127) / 128, b0 = blockIdx.y * U;
     const int64_t r = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    start_next_grid();  // the product's barriers and tensor memory are set up meanwhile
     wait_prior_grid();
     float v[U][8];
 #pragma unroll
