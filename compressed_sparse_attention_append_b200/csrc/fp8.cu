@@ -147,8 +147,7 @@ __device__ __forceinline__ void store_out(const Fp8GemmArgs& a, int64_t i, int64
         reinterpret_cast<uint16_t*>(a.out)[i * a.out_stride + j] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// two fp32 as the 64-bit operand of the packed instructions, and back (in instructions of their own: shifts of
-// a 64-bit sum make the compiler keep it as two registers and pack it again for every product)
+// two fp32 as the 64-bit operand of the packed instructions, and back
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
