@@ -11,7 +11,7 @@
 // Reading taken here: one softmax over selected and window entries, the latent serving as K and
 // V (no separate value projection), default scale 1/sqrt(512).
 //
-// One CTA per query row, 16 warps. The row's keys come in tiles of 128: ceil(k / 128) tiles of
+// One CTA per query row, 16 worker warps and one that issues the MMAs. The row's keys come in tiles of 128: ceil(k / 128) tiles of
 // selected entries (-1 or invalid entries are zero rows, masked), then one tile of up to 128 window
 // rows. Per tile:
 //   1. the tile's raw rows (loaded into registers while the previous tile was being processed) are
@@ -19,21 +19,28 @@
 //      swizzled 64-channel blocks);
 //   2. S^T = L Q^T on tcgen05 (kind::f16, M = 128 keys, N = 64 heads, K = 512), fp32 in tensor
 //      memory;
-//   3. softmax: each thread holds one key's logits for 16 heads; the tile's per-head maxima are
+//   3. softmax: each thread has one key's logits for 16 heads; the tile's per-head maxima are
 //      reduced across the CTA (a warp reduction per head, then the four lane quarters through
 //      shared memory); the running maximum m of a head moves only when the tile exceeds it
 //      by more than 8 (in log2 units), and then the head's accumulated O and l are rescaled (in
 //      tensor memory), so P = exp2(logit - m) <= 2^8 stays well inside fp16; P is rounded to fp16
-//      into shared memory, [key][head] (MN-major);
+//      into shared memory, [key][head] (MN-major). Every warp moves the maxima of its own heads, so
+//      a tile has one barrier;
 //   4. O^T += L^T P^T on tcgen05 (M = 128 channels, four M tiles, N = 64 heads, K = 128 keys): the
 //      same shared-memory bytes of L, read MN-major (channels contiguous), so the latent is
 //      dequantised once for both products.
 // The two channel halves of L (64-channel blocks 0..3 and 4..7) are dequantised one after the other,
 // each as soon as the O^T MMAs of the previous tile that read it have completed, and the
-// S^T k-steps of a half are issued as soon as that half is in place (mbarriers between the threads
-// and the MMA issuer), so dequantisation overlaps the tensor pipe. Four lanes take a key, 16 bytes each of
-// every 64 of its row: a warp's load touches 8 lines, not 32. The row's indices are checked
-// and staged in shared memory once, so no tile waits on a dependent index load.
+// S^T k-steps of a half are issued as soon as that half is in place (mbarriers between the workers
+// and the MMA warp), so dequantisation overlaps the tensor pipe. An MMA is issued only once the pipe has
+// room for it: 32 of them hold their thread for as long as they run (2,300 to 3,200 cycles), which is why
+// they have a warp of their own. With it 96 registers a thread are left, so the softmax reads its logits
+// twice instead of keeping them. Five tiles: 29.7 us a call at 128 rows, against 37.2 with the MMAs on a
+// worker and two barriers more per tile (channel quarters in place of halves 30.9; 20 warps with
+// setmaxnreg spill).
+// Four lanes take a key, 16 bytes each of every 64 of its row: a warp's load touches 8 lines, not 32; a key's
+// scales are read once, 8 a lane, and passed between its lanes. The row's indices are checked
+// and staged in shared memory once, so no tile waits on a dependent index load. Q arrives by one bulk copy.
 // Tensor memory: S^T in columns 0..63, O^T in columns 64..319 (channels on the lanes).
 // The result is normalised by the per-head sum of P at the end: out = O / l, lse = m ln 2 + ln l.
 // Every wait on the tensor cores is bounded; one that runs out sets CSA2_DEV_TIMEOUT.
@@ -46,7 +53,8 @@ namespace {
 
 using namespace tc;
 
-constexpr int kT = 512;                       // threads; loads: key tid >> 2, a quarter of its chunks each
+constexpr int kT = 512;                       // workers; loads: key tid >> 2, a quarter of its chunks each
+constexpr int kThreads = kT + 32;             // and a warp one thread of which issues the MMAs
 constexpr int kTile = 128;                    // keys per tile (MMA M of S^T)
 constexpr int kBlk = kTile * 128;             // 16384: one 64-channel block of the L tile
 constexpr int kLTile = 8 * kBlk;              // 131072: the fp16 L tile
@@ -63,13 +71,14 @@ constexpr uint32_t kIdescO = kIdescS | (1u << 15) | (1u << 16);
 constexpr size_t kOffQ = kLTile, kOffP = kOffQ + kQBytes, kOffIdx = kOffP + kPBytes;
 constexpr size_t kOffRed = kOffIdx + 4 * kMaxK;
 constexpr size_t kOffM = kOffRed + 4 * 64 * 4, kOffAl = kOffM + 64 * 4, kOffL = kOffAl + 64 * 4;
-constexpr size_t kOffBar = kOffL + 64 * 4, kOffSlot = kOffBar + 8 * 8;
+constexpr size_t kOffW = kOffL + 64 * 4, kOffBar = kOffW + (kT / 32) * 32 * 4, kOffSlot = kOffBar + 8 * 8;
 constexpr size_t kUsed = kOffSlot + 16;
 // the whole 227 KB: one CTA per SM (tensor memory and the L tile allow no second one)
 constexpr size_t kSmem = 232448;
 static_assert(kUsed + 1024 <= kSmem, "shared memory plan");
-// mbarriers: S^T done; O^T of channel half 0 / 1 done; channel half 0 / 1 of L dequantised
-enum { kBarS = 0, kBarO0 = 1, kBarO1 = 2, kBarH0 = 3, kBarH1 = 4 };
+// mbarriers: S^T done; O^T of channel half 0 / 1 done; channel half 0 / 1 of L dequantised; Q as it is in place;
+// P in place
+enum { kBarS = 0, kBarO0 = 1, kBarO1 = 2, kBarH0 = 3, kBarH1 = 4, kBarQ = 5, kBarP = 6 };
 
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, bool acc) {
     asm volatile(
@@ -107,6 +116,20 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+// 8 columns of this warp's lanes of tensor memory
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// a barrier of the worker warps alone
+__device__ __forceinline__ void workers_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kT) : "memory"); }
+
 // 16 lanes' worth of sums reduced across the warp: lane L < 16 ends with the sum over all 32 lanes
 // of element L (the transposing butterfly: each step halves the elements a lane keeps).
 __device__ __forceinline__ float warp_sum16(float (&v)[16], int lane) {
@@ -131,7 +154,7 @@ __device__ __forceinline__ float warp_sum16(float (&v)[16], int lane) {
 // 2^(m_r - m) / l, each writes its scaled O over its L tile, and each adds up its share of the heads in
 // rank order.
 template <bool PAGED>
-__global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) latent_attend_kernel(LatentAttendArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* Lt = sm;
@@ -139,8 +162,8 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     unsigned char* Ps = sm + kOffP;
     int* sidx = reinterpret_cast<int*>(sm + kOffIdx);       // the row's selected entries, -1 if unusable
     float* red = reinterpret_cast<float*>(sm + kOffRed);   // [4 lane quarters][64 heads]
-    float* s_m = reinterpret_cast<float*>(sm + kOffM);     // running maximum per head (log2 units)
-    float* s_al = reinterpret_cast<float*>(sm + kOffAl);   // this tile's rescale factor per head
+    float* s_m = reinterpret_cast<float*>(sm + kOffM);     // final maximum per head (log2 units)
+    float* s_al = reinterpret_cast<float*>(sm + kOffAl);   // final factor per head
     float* s_l = reinterpret_cast<float*>(sm + kOffL);     // final sum per head
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + kOffSlot);
@@ -152,9 +175,27 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     const int split = PAGED ? a.split : 1;
     const int rank = PAGED && split > 1 ? (int)cluster_rank() : 0;
     const int row = PAGED ? (int)(blockIdx.x / (unsigned)split) : (int)blockIdx.x, K = a.k;
-    // (takes some 3500 cycles: under way while the other warps fetch the row's position and indices)
-    if (warp == kT / 32 - 1) tmem_alloc(tslot, kCols);
+    const bool issuer = warp == kT / 32;
+    if (tid == kT) {
+        mbar_init(&bars[kBarS], 1);
+        mbar_init(&bars[kBarP], kT / 32);
+        mbar_init(&bars[kBarO0], 1);
+        mbar_init(&bars[kBarO1], 1);
+        mbar_init(&bars[kBarH0], kT / 32);
+        mbar_init(&bars[kBarH1], kT / 32);
+        mbar_init(&bars[kBarQ], 1);
+        mbar_fence_init();
+    }
     wait_prior_grid();  // indices, cache and queries come from earlier work on the stream
+    // Q goes to the L tile's place as it is, past the registers and the load path, while the row's indices are
+    // staged and tile 0's rows requested; it is converted there before the first dequantisation.
+    if (tid == kT) {
+        mbar_expect_tx(&bars[kBarQ], kQBytes);
+        bulk_g2s(Lt, a.q + (size_t)row * kLatHQ * kLatD, kQBytes, &bars[kBarQ]);
+    }
+    __syncwarp();
+    // (takes some 3500 cycles: under way while the workers fetch the row's position and indices)
+    if (issuer) tmem_alloc(tslot, kCols);
 
     const int b = row / a.tq;
     const int64_t qpos = a.qpos[row];
@@ -178,26 +219,9 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     const float scale2 = a.sm_scale * 1.4426950408889634f;  // logits in log2 units
     uint32_t* status = a.status;
 
-    if (tid == 0) {
-        mbar_init(&bars[kBarS], 1);
-        mbar_init(&bars[kBarO0], 1);
-        mbar_init(&bars[kBarO1], 1);
-        mbar_init(&bars[kBarH0], kT);
-        mbar_init(&bars[kBarH1], kT);
-        mbar_fence_init();
-    }
-    if (tid < 64) s_m[tid] = -INFINITY;
-    // Q (this thread: 16-byte chunks tid + 512 c of the row's 4096) requested first; it is converted once
-    // the row's indices are staged and tile 0's rows requested, so that the three loads overlap
-    uint4 qv[8];
-    {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)row * kLatHQ * kLatD) + tid;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) qv[c] = __ldg(src + kT * c);
-    }
     // the row's indices, checked once (an entry that is -1, not visible or out of range becomes -1)
     const int i0 = PAGED ? t0 * kTile : 0, i1 = PAGED && (t0 + nt) * kTile < K ? (t0 + nt) * kTile : K;
-    for (int i = i0 + tid; i < (row_ok ? i1 : 0); i += kT) {
+    for (int i = i0 + tid; i < (row_ok && !issuer ? i1 : 0); i += kT) {
         const int v = __ldg(a.idx + (size_t)row * K + i);
         const bool ok = v >= 0 && (int64_t)v <= qlast && (int64_t)v < a.c.cap;
         if (!ok && v != -1) set_status(status, CSA2_DEV_BAD_INDEX);
@@ -229,21 +253,20 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     // (of a window row only the first channel half: the other is loaded while it is dequantised, so that no
     // more than 18 registers of raw data stay live across the softmax of the tile before)
     uint4 raw[4];
-    uint32_t rsc[2];  // two scales per c
+    uint2 rsc;  // eight scales: those of channels 128 qq .. (the four lanes of a key hold each other's)
     auto load_tile = [&](int j) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-        rsc[0] = rsc[1] = 0u;
+        rsc = make_uint2(0, 0);
         if (j < nt && t0 + j < ft) {  // (the indices of this CTA's tiles are staged, no others)
             const int i = (t0 + j) * kTile + lkey;
             const int v = i < K ? sidx[i] : -1;
             if (v >= 0) {
                 const uint4* src = reinterpret_cast<const uint4*>(a.c.l_data + (seq_row0 + (size_t)v) * kLatBytes) + qq;
-                const uint16_t* sc = reinterpret_cast<const uint16_t*>(a.c.l_scale + (seq_row0 + (size_t)v) * kLatScales) + qq;
+                const uint2* sc = reinterpret_cast<const uint2*>(a.c.l_scale + (seq_row0 + (size_t)v) * kLatScales) + qq;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) raw[c] = __ldg(src + 4 * c);
-                rsc[0] = (uint32_t)__ldg(sc) | ((uint32_t)__ldg(sc + 4) << 16);
-                rsc[1] = (uint32_t)__ldg(sc + 8) | ((uint32_t)__ldg(sc + 12) << 16);
+                rsc = __ldg(sc);
             }
         } else if (j < nt && lkey < nwin) {
 #pragma unroll
@@ -265,8 +288,10 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
                 const bool far = qq >= 2;
                 const uint32_t w[4] = {far ? raw[c].z : raw[c].x, far ? raw[c].w : raw[c].y, far ? raw[c].x : raw[c].z,
                                        far ? raw[c].y : raw[c].w};
-                const uint32_t s16 = (rsc[c >> 1] >> (16 * (c & 1))) & 0xFFFFu, first = far ? s16 >> 8 : s16 & 0xFFu,
-                               second = far ? s16 & 0xFFu : s16 >> 8;
+                // this lane's two scales are bytes 2 qq, 2 qq + 1 of those that the key's lane c holds
+                const uint32_t lo4 = __shfl_sync(0xffffffffu, rsc.x, c, 4), hi4 = __shfl_sync(0xffffffffu, rsc.y, c, 4);
+                const uint32_t s16 = (far ? hi4 : lo4) >> (16 * (qq & 1));
+                const uint32_t first = (far ? s16 >> 8 : s16) & 0xFFu, second = (far ? s16 : s16 >> 8) & 0xFFu;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {  // 8 channels; two code words share a scale
                     const uint32_t s2 = scale_h2(i < 2 ? first : second);
@@ -295,13 +320,16 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
         }
     };
 
-    __syncthreads();  // barriers, s_m, indices
-    load_tile(0);
-    {   // Q -> fp16 (B operand of S^T, K-major: row = head, 64-channel blocks)
+    __syncthreads();  // barriers, indices
+    if (!issuer) {
+        load_tile(0);
+        wait_bar(kBarQ, 0);
+        // Q -> fp16 (B operand of S^T, K-major: row = head, 64-channel blocks)
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             const int g = tid + kT * c, h = g >> 6, ch = g & 63;  // head, 8-channel chunk
-            const uint32_t w[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
+            const uint4 qv = reinterpret_cast<const uint4*>(Lt)[g];
+            const uint32_t w[4] = {qv.x, qv.y, qv.z, qv.w};
             uint32_t hv[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) hv[i] = pack_h2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
@@ -322,8 +350,40 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     // Per tile j: each channel half of L is dequantised as soon as the O^T MMAs of tile j - 1 that read it
     // have completed (O^T m-tiles 0, 1 read half 0, m-tiles 2, 3 half 1), and the S^T k-steps of a half are
     // issued as soon as the half is in shared memory, so that dequantisation overlaps the tensor pipe.
-    // The softmax then runs on all 16 warps.
-    for (int j = 0; j < nt; ++j) {
+    // The softmax then runs on the 16 worker warps.
+    if (tid == kT) {  // the MMAs
+        // (operand addresses are in the descriptors' low bits, in units of 16 bytes)
+        const uint64_t sl = sw128_desc(smem_u32(Lt)), sq = sw128_desc(smem_u32(Qs)), sp = sw128_desc_mn(smem_u32(Ps), 0);
+        constexpr uint64_t lbo = (uint64_t)(kBlk >> 4) << 16;
+        for (int j = 0; j < nt; ++j) {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                wait_bar(hh ? kBarH1 : kBarH0, (uint32_t)j & 1u);
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 16 * hh; kk < 16 * hh + 16; ++kk)
+                    mma_f16(tb + kSCol, sl + ((kk >> 2) * kBlk + 32 * (kk & 3)) / 16, sq + ((kk >> 2) * kQBlk + 32 * (kk & 3)) / 16,
+                            kIdescS, kk > 0);
+            }
+            mma_commit(&bars[kBarS]);
+            wait_bar(kBarP, (uint32_t)j & 1u);
+            tc_fence_after();
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+                // A = L^T: channels 128 mt .. (blocks 2 mt, 2 mt + 1, kBlk apart), keys 16 kk ..;
+                // B = P: heads 0..63 (one 64-element group), keys 16 kk ..
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_f16(tb + kOCol + 64 * mt, sl + lbo + (2 * mt * kBlk >> 4) + 128 * kk, sp + 128 * kk, kIdescO, j > 0 || kk > 0);
+                if (mt == 1) mma_commit(&bars[kBarO0]);  // channel half 0 of L is free again
+            }
+            mma_commit(&bars[kBarO1]);
+        }
+    }
+    __syncwarp();
+    float m_run = -INFINITY;  // running maximum of head 16 cg + (lane & 15) (log2 units)
+    float* wm = reinterpret_cast<float*>(sm + kOffW) + 32 * warp;  // this warp's maxima and rescale factors
+    for (int j = 0; j < (issuer ? 0 : nt); ++j) {
         const bool fp4 = t0 + j < ft;  // CTA-uniform
         const bool more = lkey < nwin;
         const bool valid = key_valid(j);
@@ -332,107 +392,84 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
             if (j > 0) wait_bar(hh ? kBarO1 : kBarO0, (uint32_t)(j - 1) & 1u);
             dequant(hh, fp4, more);
             fence_async_smem();
-            mbar_arrive(&bars[hh ? kBarH1 : kBarH0]);
-            if (hh == 1 && j + 1 < nt) load_tile(j + 1);  // in flight during this tile's MMAs and softmax
-            if (tid == 0) {
-                wait_bar(hh ? kBarH1 : kBarH0, (uint32_t)j & 1u);
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 16 * hh; kk < 16 * hh + 16; ++kk) {
-                    const uint32_t off = (uint32_t)((kk >> 2) * kBlk + 32 * (kk & 3));
-                    const uint32_t qoff = (uint32_t)((kk >> 2) * kQBlk + 32 * (kk & 3));
-                    mma_f16(tb + kSCol, sw128_desc(smem_u32(Lt) + off), sw128_desc(smem_u32(Qs) + qoff), kIdescS, kk > 0);
-                }
-                if (hh == 1) mma_commit(&bars[kBarS]);
-            }
             __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[hh ? kBarH1 : kBarH0]);
         }
+        if (j + 1 < nt) load_tile(j + 1);  // in flight during this tile's MMAs and softmax
         wait_bar(kBarS, (uint32_t)j & 1u);  // also every earlier MMA (the O^T of tile j - 1)
         tc_fence_after();
 
         // ---- softmax of the tile: this thread's key 32 quad + lane (= key), heads 16 cg .. +15 ----
-        float lg[16];  // raw logits q . l (the scale is applied inside the exponent)
-        {
+        {  // (raw logits q . l: the scale is applied inside the exponent)
             uint32_t v[16];
             tmem_ld16(tb + lane_base + kSCol + 16 * cg, v);
             tmem_ld_wait();
-            float r[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                lg[i] = __uint_as_float(v[i]);
-                r[i] = warp_max(valid ? lg[i] * scale2 : -INFINITY);  // (any sign of the scale)
-            }
-            if (lane == 0) {
-                float4* d = reinterpret_cast<float4*>(red + quad * 64 + 16 * cg);
-                d[0] = make_float4(r[0], r[1], r[2], r[3]);
-                d[1] = make_float4(r[4], r[5], r[6], r[7]);
-                d[2] = make_float4(r[8], r[9], r[10], r[11]);
-                d[3] = make_float4(r[12], r[13], r[14], r[15]);
+            for (int i = 0; i < 16; i += 4) {
+                float r[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // (any sign of the scale)
+                    r[k] = warp_max(valid ? __uint_as_float(v[i + k]) * scale2 : -INFINITY);
+                if (lane == 0) *reinterpret_cast<float4*>(red + quad * 64 + 16 * cg + i) = make_float4(r[0], r[1], r[2], r[3]);
             }
         }
-        __syncthreads();
-        int resc = 0;
-        if (tid < 64) {
-            const float tmax = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid]));
-            const float m_old = s_m[tid];
+        workers_sync();
+        // every warp moves the maxima of its heads itself (the same in the four warps that have them)
+        {
+            const float* rd = red + 16 * cg + (lane & 15);
+            const float tmax = fmaxf(fmaxf(rd[0], rd[64]), fmaxf(rd[128], rd[192]));
             float al = 1.f;
-            if (tmax > m_old + kLazy) {  // also the first finite maximum (m_old = -inf)
-                al = (m_old == -INFINITY) ? 0.f : exp2f(m_old - tmax);
-                resc = m_old != -INFINITY;
-                s_m[tid] = tmax;
+            bool moved = false;
+            if (tmax > m_run + kLazy) {  // also the first finite maximum (m_run = -inf: nothing is summed yet)
+                moved = m_run != -INFINITY;
+                if (moved) al = exp2f(m_run - tmax);
+                m_run = tmax;
             }
-            s_al[tid] = al;
-        }
-        resc = __syncthreads_or(resc);
-        const float* al = s_al + 16 * cg;  // this warp's heads (shared-memory broadcasts)
-        const float* mh = s_m + 16 * cg;
-        if (resc) {
-            // every O^T MMA so far has completed (the S^T commit tracks them): scale in place
+            wm[lane] = lane < 16 ? m_run : al;
+            const bool resc = __any_sync(0xffffffffu, moved);
+            __syncwarp();
+            if (resc) {
+                // every O^T MMA so far has completed (the S^T commit tracks them): scale in place
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                uint32_t v[16];
-                const uint32_t addr = tb + lane_base + kOCol + 64 * mt + 16 * cg;
-                tmem_ld16(addr, v);
-                tmem_ld_wait();
+                for (int o = 0; o < 16; o += 8) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * al[i]);
-                tmem_st16(addr, v);
+                    for (int mt = 0; mt < 4; ++mt) {
+                        uint32_t v[8];
+                        const uint32_t addr = tb + lane_base + kOCol + 64 * mt + 16 * cg + o;
+                        tmem_ld8(addr, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * wm[16 + o + i]);
+                        tmem_st8(addr, v);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) lsum[i] *= wm[16 + i];
+                tmem_st_wait();
             }
-            tmem_st_wait();
         }
         // a valid key makes every head's maximum finite, so p needs no test of m for -inf
-        uint32_t ph[8];
+        // (the logits are read again: registers to keep them are not there)
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            const float p0 = valid ? ex2(fmaf(lg[i], scale2, -mh[i])) : 0.f;
-            const float p1 = valid ? ex2(fmaf(lg[i + 1], scale2, -mh[i + 1])) : 0.f;
-            lsum[i] = fmaf(lsum[i], al[i], p0);
-            lsum[i + 1] = fmaf(lsum[i + 1], al[i + 1], p1);
-            ph[i >> 1] = pack_h2(p0, p1);
+        for (int o = 0; o < 16; o += 8) {
+            uint32_t v[8], ph[4];
+            tmem_ld8(tb + lane_base + kSCol + 16 * cg + o, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float p0 = valid ? ex2(fmaf(__uint_as_float(v[i]), scale2, -wm[o + i])) : 0.f;
+                const float p1 = valid ? ex2(fmaf(__uint_as_float(v[i + 1]), scale2, -wm[o + i + 1])) : 0.f;
+                lsum[o + i] += p0;
+                lsum[o + i + 1] += p1;
+                ph[i >> 1] = pack_h2(p0, p1);
+            }
+            // P [key][head]: heads 16 cg .. +7 -> chunk 2 cg, 16 cg + 8 .. -> chunk 2 cg + 1
+            *reinterpret_cast<uint4*>(Ps + sw(key, 2 * cg + o / 8)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
         }
-        // P [key][head]: heads 16 cg .. +7 -> chunk 2 cg, 16 cg + 8 .. -> chunk 2 cg + 1
-        *reinterpret_cast<uint4*>(Ps + sw(key, 2 * cg)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-        *reinterpret_cast<uint4*>(Ps + sw(key, 2 * cg + 1)) = make_uint4(ph[4], ph[5], ph[6], ph[7]);
         fence_async_smem();
         tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {
-            tc_fence_after();
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    // A = L^T: channels 128 mt .. (blocks 2 mt, 2 mt + 1, kBlk apart), keys 16 kk ..
-                    const uint64_t ad = sw128_desc_mn(smem_u32(Lt) + (uint32_t)(2 * mt * kBlk + 2048 * kk), kBlk);
-                    // B = P: heads 0..63 (one 64-element group), keys 16 kk ..
-                    const uint64_t bd = sw128_desc_mn(smem_u32(Ps) + (uint32_t)(2048 * kk), 0);
-                    mma_f16(tb + kOCol + 64 * mt, ad, bd, kIdescO, j > 0 || kk > 0);
-                }
-                if (mt == 1) mma_commit(&bars[kBarO0]);  // channel half 0 of L is free again
-            }
-            mma_commit(&bars[kBarO1]);
-        }
         __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarP]);
     }
     if (nt > 0) {
         wait_bar(kBarO1, (uint32_t)(nt - 1) & 1u);  // the last MMAs (in issue order)
@@ -440,9 +477,10 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     }
 
     // ---- epilogue: l per head, then out = O / l (warp: channels 128 mt + 32 quad + lane, heads 16 cg ..) ----
-    {
+    if (!issuer) {
         const float r = warp_sum16(lsum, lane);
         if (lane < 16) red[quad * 64 + 16 * cg + lane] = r;
+        if (quad == 0 && lane < 16) s_m[16 * cg + lane] = m_run;
     }
     __syncthreads();
     if (PAGED && split > 1) {
@@ -465,7 +503,7 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
         // every MMA that reads L has completed: O goes there as fp32 [head][512]
         float* part = reinterpret_cast<float*>(Lt);
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
+        for (int mt = 0; mt < (issuer ? 0 : 4); ++mt) {
             uint32_t v[16] = {};
             if (nt > 0) {
                 tmem_ld16(tb + lane_base + kOCol + 64 * mt + 16 * cg, v);
@@ -480,7 +518,7 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
         __syncthreads();
         cluster_sync();
         const int e0 = kLatHQ * rank / split * kLatD, e1 = kLatHQ * (rank + 1) / split * kLatD;
-        for (int e = e0 + 4 * tid; e < e1; e += 4 * kT) {
+        for (int e = e0 + 4 * tid; e < (issuer ? 0 : e1); e += 4 * kT) {
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int r = 0; r < split; ++r) {
                 const float4 x = ld_cluster4(smem_u32(part + e), r);
@@ -496,7 +534,7 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if (warp == kT / 32 - 1) tmem_dealloc(tb, kCols);
+        if (issuer) tmem_dealloc(tb, kCols);
         return;
     }
     if (tid < 64) {
@@ -507,7 +545,7 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     }
     __syncthreads();
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
+    for (int mt = 0; mt < (issuer ? 0 : 4); ++mt) {
         uint32_t v[16] = {};
         if (nt > 0) {
             tmem_ld16(tb + lane_base + kOCol + 64 * mt + 16 * cg, v);
@@ -529,7 +567,7 @@ __global__ void __launch_bounds__(kT, 1) latent_attend_kernel(LatentAttendArgs a
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kT / 32 - 1) tmem_dealloc(tb, kCols);
+    if (issuer) tmem_dealloc(tb, kCols);
 }
 
 }  // namespace
@@ -542,10 +580,10 @@ static cudaError_t launch_rows(const LatentAttendArgs& a, int split, cudaStream_
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     if (a.rows == 0) return cudaSuccess;
-    if (split == 1) return launch_after_prior(k, dim3((unsigned)a.rows), dim3(kT), kSmem, s, a);
+    if (split == 1) return launch_after_prior(k, dim3((unsigned)a.rows), dim3(kThreads), kSmem, s, a);
     if (split > 8) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    return launch_cluster(k, dim3((unsigned)(a.rows * split)), dim3(kT), split, kSmem, s, a);
+    return launch_cluster(k, dim3((unsigned)(a.rows * split)), dim3(kThreads), split, kSmem, s, a);
 }
 
 cudaError_t launch_latent_attend(const LatentAttendArgs& a, cudaStream_t s) { return launch_rows<false>(a, 1, s); }
