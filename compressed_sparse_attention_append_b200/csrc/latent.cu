@@ -35,7 +35,7 @@
 // and the MMA warp), so dequantisation overlaps the tensor pipe. An MMA is issued only once the pipe has
 // room for it: 32 of them hold their thread for as long as they run (2,300 to 3,200 cycles), which is why
 // they have a warp of their own. With it 96 registers a thread are left, so the softmax reads its logits
-// twice instead of keeping them. Five tiles: 29.7 us a call at 128 rows, against 37.2 with the MMAs on a
+// twice instead of keeping them. Five tiles at 128 rows: 29.7 us a call, against 37.2 with the MMAs on a
 // worker and two barriers more per tile (channel quarters in place of halves 30.9; 20 warps with
 // setmaxnreg spill).
 // Four lanes take a key, 16 bytes each of every 64 of its row: a warp's load touches 8 lines, not 32; a key's
@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_kernel(LatentAttend
         mbar_init(&bars[kBarQ], 1);
         mbar_fence_init();
     }
+    start_next_grid();  // (0.5 us less in a run of calls: the next launch is set up beside this one)
     wait_prior_grid();  // indices, cache and queries come from earlier work on the stream
     // Q goes to the L tile's place as it is, past the registers and the load path, while the row's indices are
     // staged and tile 0's rows requested; it is converted there before the first dequantisation.
@@ -197,32 +198,33 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_kernel(LatentAttend
     // (takes some 3500 cycles: under way while the workers fetch the row's position and indices)
     if (issuer) tmem_alloc(tslot, kCols);
 
+    // the row's tiles, of which this CTA has t0 .. t0 + nt - 1
     const int b = row / a.tq;
-    const int64_t qpos = a.qpos[row];
-    const int64_t qlast = qpos < 0 ? -1 : (qpos + 1) / a.ratio - 1;  // the last visible entry
+    const int ft = (K + kTile - 1) / kTile, all = ft + (a.win > 0 ? 1 : 0);
+    const int t0 = PAGED ? all * rank / split : 0, t1 = PAGED ? all * (rank + 1) / split : all;
+    const int i0 = t0 * kTile, i1 = t1 * kTile < K ? t1 * kTile : K;
+    // (the loads that wait for nothing are all under way before the first of them is used)
+    const int first = !issuer && i0 + tid < i1 ? __ldg(a.idx + (size_t)row * K + i0 + tid) : -1;
+    const int64_t qpos = __ldg(a.qpos + row);
+    const int64_t sb = __ldg(a.swa_begin ? a.swa_begin + b : a.qpos + row);  // (no branch: it would keep the next load back)
+    int64_t ring = b;  // the window ring of this row
+    if constexpr (PAGED) ring = a.win > 0 ? paged_slot(a.pg, b) : -1;
+    const int64_t qlast = ((qpos + 1) >> (a.ratio - 1)) - 1;  // the last visible entry (below 0 for qpos < 0)
     // (a page table bounds its own entries, each index is checked against it: the window needs none of them)
     const bool row_ok = qpos >= 0 && (PAGED || qlast < a.c.cap);
     int64_t lo = qpos - a.win + 1;
-    {
-        const int64_t sb = a.swa_begin ? a.swa_begin[b] : 0;
-        if (lo < sb) lo = sb;
-        if (lo < 0) lo = 0;
-    }
-    int64_t ring = b;  // the window ring of this row
-    if constexpr (PAGED) ring = a.win > 0 ? paged_slot(a.pg, b) : -1;
-    if (PAGED && ring < 0 && a.win > 0 && threadIdx.x == 0) set_status(a.status, CSA2_DEV_BAD_PAGE);
+    if (a.swa_begin && lo < sb) lo = sb;
+    if (lo < 0) lo = 0;
+    if (PAGED && ring < 0 && a.win > 0 && tid == 0) set_status(a.status, CSA2_DEV_BAD_PAGE);
     const int nwin = (row_ok && qpos >= lo && (!PAGED || ring >= 0)) ? (int)(qpos - lo + 1) : 0;
-    const int ft = row_ok ? (K + kTile - 1) / kTile : 0;
-    const int all = ft + (nwin > 0 ? 1 : 0);                // the row's tiles; this CTA's: t0 .. t0 + nt - 1
-    const int t0 = PAGED ? all * rank / split : 0;
-    const int nt = PAGED ? all * (rank + 1) / split - t0 : all;
+    int nt = row_ok ? t1 - t0 : 0;
+    if (nt > 0 && t1 > ft && nwin == 0) --nt;
     const float scale2 = a.sm_scale * 1.4426950408889634f;  // logits in log2 units
     uint32_t* status = a.status;
 
     // the row's indices, checked once (an entry that is -1, not visible or out of range becomes -1)
-    const int i0 = PAGED ? t0 * kTile : 0, i1 = PAGED && (t0 + nt) * kTile < K ? (t0 + nt) * kTile : K;
     for (int i = i0 + tid; i < (row_ok && !issuer ? i1 : 0); i += kT) {
-        const int v = __ldg(a.idx + (size_t)row * K + i);
+        const int v = i == i0 + tid ? first : __ldg(a.idx + (size_t)row * K + i);
         const bool ok = v >= 0 && (int64_t)v <= qlast && (int64_t)v < a.c.cap;
         if (!ok && v != -1) set_status(status, CSA2_DEV_BAD_INDEX);
         if constexpr (PAGED) {
@@ -551,13 +553,18 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_kernel(LatentAttend
             tmem_ld16(tb + lane_base + kOCol + 64 * mt + 16 * cg, v);
             tmem_ld_wait();
         }
-        const int d = 128 * mt + 32 * quad + lane;
+        // lanes 2 i and 2 i + 1 exchange halves of their heads: a lane ends with a pair of channels of every second
+        // head (half the stores; 28.8 us at 128 rows against 29.3, four channels a lane 29.6)
+        const int d = 128 * mt + 32 * quad + (lane & 30), odd = lane & 1;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float x = __uint_as_float(v[i]) * s_al[16 * cg + i];
-            const size_t ob = ((size_t)row * kLatHQ + 16 * cg + i) * kLatD + d;
-            a.out[ob] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-            if (a.out_f32) a.out_f32[ob] = x;
+        for (int i = 0; i < 16; i += 2) {
+            const float x0 = __uint_as_float(v[i]) * s_al[16 * cg + i], x1 = __uint_as_float(v[i + 1]) * s_al[16 * cg + i + 1];
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 1);
+            const float2 o = odd ? make_float2(got, x1) : make_float2(x0, got);
+            const size_t ob = ((size_t)row * kLatHQ + 16 * cg + i + odd) * kLatD + d;
+            const __nv_bfloat162 h = __floats2bfloat162_rn(o.x, o.y);
+            *reinterpret_cast<__nv_bfloat162*>(a.out + ob) = h;
+            if (a.out_f32) *reinterpret_cast<float2*>(a.out_f32 + ob) = o;
         }
     }
     if (a.lse && tid < 64) {
@@ -589,7 +596,7 @@ static cudaError_t launch_rows(const LatentAttendArgs& a, int split, cudaStream_
 cudaError_t launch_latent_attend(const LatentAttendArgs& a, cudaStream_t s) { return launch_rows<false>(a, 1, s); }
 
 cudaError_t launch_paged_attend(LatentAttendArgs a, cudaStream_t s) {
-    // A tile takes about 4.6 us, what surrounds them 11 and the join 2: a row's tiles go over as many CTAs
+    // A tile takes about 3.5 us, what surrounds them 11 and the join 2: a row's tiles go over as many CTAs
     // as leave every row's cluster on the GPU at once. How many of a size fit next to one another is a
     // matter of the SMs per GPC (a second round of clusters costs more than the split gains).
     constexpr struct { int size, rows; } kFit[] = {{16, 6}, {8, 14}, {6, 20}, {5, 24}, {4, 30}, {3, 42}, {2, 72}};
