@@ -1,7 +1,9 @@
 """Binding of include/csa2_layer.h: the operators around the CSA2 core. Argument marshalling only, in the
 manner of the package's other calls (same names as the C entry points, tensors for pointers, the
 current CUDA stream, Csa2Error on a non-zero status, no CPU fallback). Every tensor of a call lies on the
-current device.
+current device. A call as it should be goes through csrc/marshal.cpp (3.2 us of host time with the launch,
+against 6 to 8 through ctypes); whatever that does not take comes back and is done, or refused with its reason,
+by the code below.
 
 One decode step of a layer of the pages' own shape, `B` sequences (bf16 unless noted):
 
@@ -149,12 +151,21 @@ assert struct.calcsize("@PqqPP") == ctypes.sizeof(csa2_append_row)
 
 
 _lib = None
+_fast = None  # csrc/marshal.cpp: the checks and the call of the plain cases in native code, once the library is loaded
 
 
 def _load():
     """The library, kept here after the first call."""
-    global _lib
+    global _lib, _fast
     _lib = lib()
+    try:
+        from . import _marshal
+    except ImportError:  # not built here: the calls below are complete without it
+        return _lib
+    if torch.__version__.split("+")[0] == _marshal.torch_version:
+        names = ("rope", "norm_rope", "fp8_quantize", "fp8_gemm", "paged_append", "paged_gather", "paged_attend")
+        _marshal.bind(*(ctypes.cast(getattr(_lib, "csa2_" + n), ctypes.c_void_p).value for n in names))
+        _fast = _marshal
     return _lib
 
 
@@ -209,40 +220,60 @@ def _heads(x, out, weight, dtype, dev, tokens, d):
 
 def csa2_rope(rope: Rope, pos, x, out, stream=None):
     """x [tokens, heads, d] bf16 or fp32 (any strides, dense heads) -> out (may be x), pos [tokens] int64."""
+    s = _fast and _fast.rope(rope.at, pos, x, out, stream)
+    if s is None:
+        s = _rope(rope, pos, x, out, stream)
+    if s:
+        raise Csa2Error("csa2_rope", s)
+
+
+def _rope(rope, pos, x, out, stream):
     tokens, _, d = x.shape
     dtype, dev = x.dtype, _device()
     assert dtype in _TYPES, "expected a bf16 or fp32 tensor"
     h = _heads(x, out, None, dtype, dev, tokens, d)
-    s = (_lib or _load()).csa2_rope(rope.ref, _TYPES[dtype], tokens, d, _ptr(pos, _I64, dev, (tokens,)), h,
-                        _stream(stream, dev))
-    if s:
-        raise Csa2Error("csa2_rope", s)
+    return (_lib or _load()).csa2_rope(
+        rope.ref, _TYPES[dtype], tokens, d, _ptr(pos, _I64, dev, (tokens,)), h, _stream(stream, dev))
 
 
 def csa2_norm_rope(rope, pos, eps, q, wq, q_out, k=None, wk=None, k_out=None, stream=None):
     """q [tokens, hq, d] and k [tokens, hk, d] (or None) normed per head with weights wq, wk [d] (or None) and
     rotated (rope None: the norm alone) -> q_out, k_out (may be q, k)."""
+    s = _fast and _fast.norm_rope(None if rope is None else rope.at, pos, eps, q, wq, q_out, k, wk, k_out, stream)
+    if s is None:
+        s = _norm_rope(rope, pos, eps, q, wq, q_out, k, wk, k_out, stream)
+    if s:
+        raise Csa2Error("csa2_norm_rope", s)
+
+
+def _norm_rope(rope, pos, eps, q, wq, q_out, k, wk, k_out, stream):
     tokens, _, d = q.shape
     dtype, dev = q.dtype, _device()
     assert dtype in _TYPES, "expected a bf16 or fp32 tensor"
     hq = _heads(q, q_out, wq, dtype, dev, tokens, d)
     hk = None if k is None else _heads(k, k_out, wk, dtype, dev, tokens, d)
-    s = (_lib or _load()).csa2_norm_rope(None if rope is None else rope.ref, _TYPES[dtype], tokens, d,
-                             _ptr(pos, _I64, dev, (tokens,)), eps, hq, hk, _stream(stream, dev))
-    if s:
-        raise Csa2Error("csa2_norm_rope", s)
+    return (_lib or _load()).csa2_norm_rope(
+        None if rope is None else rope.ref, _TYPES[dtype], tokens, d, _ptr(pos, _I64, dev, (tokens,)), eps, hq, hk,
+        _stream(stream, dev))
 
 
 def csa2_fp8_quantize(x, data, scale, stream=None):
     """x [rows, k] bf16 (dense rows) -> data [rows, k] E4M3 (or uint8), scale [ceil(k / 128), rows] fp32."""
+    s = _fast and _fast.quantize(x, data, scale, stream)
+    if s is None:
+        s = _fp8_quantize(x, data, scale, stream)
+    if s:
+        raise Csa2Error("csa2_fp8_quantize", s)
+
+
+def _fp8_quantize(x, data, scale, stream):
     rows, k = x.shape
     xs, one = x.stride()
     dev = _device()
     assert one == 1 or k == 1, "expected dense rows"
-    s = (_lib or _load()).csa2_fp8_quantize(rows, k, _strided(x, _BF16, dev, (rows, k)), xs, _ptr(data, _E4M3, dev, (rows, k)),
-                                _ptr(scale, _F32, dev, (-(-k // 128), rows)), _stream(stream, dev))
-    if s:
-        raise Csa2Error("csa2_fp8_quantize", s)
+    return (_lib or _load()).csa2_fp8_quantize(
+        rows, k, _strided(x, _BF16, dev, (rows, k)), xs, _ptr(data, _E4M3, dev, (rows, k)),
+        _ptr(scale, _F32, dev, (-(-k // 128), rows)), _stream(stream, dev))
 
 
 def csa2_fp8_quantize_weight(w, data, scale, stream=None):
@@ -257,17 +288,24 @@ def csa2_fp8_quantize_weight(w, data, scale, stream=None):
 def csa2_fp8_gemm(x, xs, w, ws, out, status=None, stream=None):
     """out [m, n] (bf16 or fp32, dense rows) = x [m, k] w [n, k]^T, E4M3 with the scales of csa2_fp8_quantize (xs)
     and csa2_fp8_quantize_weight (ws); status: a workspace for CSA2_DEV_TIMEOUT."""
+    at, size = _status(status)
+    s = _fast and _fast.gemm(x, xs, w, ws, out, at, size, stream)
+    if s is None:
+        s = _fp8_gemm(x, xs, w, ws, out, at, size, stream)
+    if s:
+        raise Csa2Error("csa2_fp8_gemm", s)
+
+
+def _fp8_gemm(x, xs, w, ws, out, at, size, stream):
     m, k = x.shape
     n, nb, dev, dtype = w.shape[0], -(-k // 128), _device(), out.dtype
     o0, o1 = out.stride()
     assert dtype in _TYPES, "expected a bf16 or fp32 tensor"
     assert o1 == 1 or n == 1, "expected dense rows"
-    at, size = _status(status)
-    s = (_lib or _load()).csa2_fp8_gemm(m, n, k, _ptr(x, _E4M3, dev, (m, k)), _ptr(xs, _F32, dev, (nb, m)), _ptr(w, _E4M3, dev, (n, k)),
-                            _ptr(ws, _F32, dev, (-(-n // 128), nb)), _TYPES[dtype],
-                            _strided(out, dtype, dev, (m, n)), o0 if o0 > n else n, at, size, _stream(stream, dev))
-    if s:
-        raise Csa2Error("csa2_fp8_gemm", s)
+    return (_lib or _load()).csa2_fp8_gemm(
+        m, n, k, _ptr(x, _E4M3, dev, (m, k)), _ptr(xs, _F32, dev, (nb, m)), _ptr(w, _E4M3, dev, (n, k)),
+        _ptr(ws, _F32, dev, (-(-n // 128), nb)), _TYPES[dtype], _strided(out, dtype, dev, (m, n)), o0 if o0 > n else n, at,
+        size, _stream(stream, dev))
 
 
 class PagedCache:
@@ -298,7 +336,7 @@ class PagedCache:
             _ptr(swa_slot, _I32, dev, (batch,)), n_pages, max_pages, n_slots, swa_cap, page)
         self.dev = dev
         self.ref = ctypes.byref(self.c)
-
+        self.at = ctypes.addressof(self.c)
 
     def on(self, batch):
         """The current device, which has to be the cache's, for a call of `batch` sequences."""
@@ -324,41 +362,69 @@ def csa2_paged_append(cache: PagedCache, batch, t, pos, latent=None, idx_k=None,
     entries pos [B] int64, normed with the weights that are given and rotated (`rope` latent and window rows,
     unless swa_rope is given, `idx_rope` the key); length [B] int32: tokens of each sequence (None: t);
     rpos [B, t] int64: the tokens' positions for the rotation (None: those of the entries)."""
-    dev = cache.on(batch)
     at, size = _status(ws)
-    s = (_lib or _load()).csa2_paged_append(
-        cache.ref, batch, t, _ptr(pos, _I64, dev, (batch,)), _ptr(length, _I32, dev, (batch,)),
-        _ptr(rpos, _I64, dev, (batch, t)), eps, _append_row(latent, w_latent, rope, dev, batch, t, 512),
-        _append_row(idx_k, w_idx_k, idx_rope, dev, batch, t, 128),
-        _append_row(swa, w_swa, rope if swa_rope is None else swa_rope, dev, batch, t, 512), at, size,
-        _stream(stream, dev))
+    if swa_rope is None:
+        swa_rope = rope
+    turn = None if rope is None else rope.at
+    s = _fast and _fast.append(
+        cache.at, cache.dev, cache.batch, batch, t, pos, length, rpos, eps, latent, w_latent, turn, idx_k, w_idx_k,
+        None if idx_rope is None else idx_rope.at, swa, w_swa, turn if swa_rope is rope else swa_rope.at, at, size, stream)
+    if s is None:
+        s = _paged_append(cache, batch, t, pos, latent, idx_k, swa, rope, idx_rope, swa_rope, w_latent, w_idx_k, w_swa, eps,
+                          length, rpos, at, size, stream)
     if s:
         raise Csa2Error("csa2_paged_append", s)
 
 
+def _paged_append(cache, batch, t, pos, latent, idx_k, swa, rope, idx_rope, swa_rope, w_latent, w_idx_k, w_swa, eps,
+                  length, rpos, at, size, stream):
+    dev = cache.on(batch)
+    return (_lib or _load()).csa2_paged_append(
+        cache.ref, batch, t, _ptr(pos, _I64, dev, (batch,)), _ptr(length, _I32, dev, (batch,)),
+        _ptr(rpos, _I64, dev, (batch, t)), eps, _append_row(latent, w_latent, rope, dev, batch, t, 512),
+        _append_row(idx_k, w_idx_k, idx_rope, dev, batch, t, 128),
+        _append_row(swa, w_swa, swa_rope, dev, batch, t, 512), at, size,
+        _stream(stream, dev))
+
+
 def csa2_paged_gather(cache: PagedCache, batch, idx, latent=None, key=None, ws=None, stream=None):
     """idx [B, n] int32 entries (-1: zeros) -> latent [B, n, 512] and key [B, n, 128] bf16 (either may be None)."""
-    dev, n = cache.on(batch), idx.shape[1]
     at, size = _status(ws)
-    s = (_lib or _load()).csa2_paged_gather(cache.ref, batch, n, _ptr(idx, _I32, dev, (batch, n)),
-                                _ptr(latent, _BF16, dev, (batch, n, 512)), _ptr(key, _BF16, dev, (batch, n, 128)), at,
-                                size, _stream(stream, dev))
+    s = _fast and _fast.gather(cache.at, cache.dev, cache.batch, batch, idx, latent, key, at, size, stream)
+    if s is None:
+        s = _paged_gather(cache, batch, idx, latent, key, at, size, stream)
     if s:
         raise Csa2Error("csa2_paged_gather", s)
+
+
+def _paged_gather(cache, batch, idx, latent, key, at, size, stream):
+    dev, n = cache.on(batch), idx.shape[1]
+    return (_lib or _load()).csa2_paged_gather(
+        cache.ref, batch, n, _ptr(idx, _I32, dev, (batch, n)), _ptr(latent, _BF16, dev, (batch, n, 512)),
+        _ptr(key, _BF16, dev, (batch, n, 128)), at, size, _stream(stream, dev))
 
 
 def csa2_paged_attend(cache: PagedCache, batch, tq, qpos, q, idx, k, out, swa_begin=None, win=128, ratio=1,
                       sm_scale=0.0, out_f32=None, lse=None, ws=None, stream=None):
     """q [B*tq, 64, 512] bf16, idx [B*tq, k] int32 -> out [B*tq, 64, 512] bf16 (tensor cores)."""
-    dev, rows = cache.on(batch), batch * tq
     at, size = _status(ws)
-    s = (_lib or _load()).csa2_paged_attend(
+    s = _fast and _fast.attend(cache.at, cache.dev, cache.batch, batch, tq, qpos, q, idx, k, swa_begin, win, ratio, sm_scale,
+                               out, out_f32, lse, at, size, stream)
+    if s is None:
+        s = _paged_attend(cache, batch, tq, qpos, q, idx, k, out, swa_begin, win, ratio, sm_scale, out_f32, lse, at, size,
+                          stream)
+    if s:
+        raise Csa2Error("csa2_paged_attend", s)
+
+
+def _paged_attend(cache, batch, tq, qpos, q, idx, k, out, swa_begin, win, ratio, sm_scale, out_f32, lse, at, size,
+                  stream):
+    dev, rows = cache.on(batch), batch * tq
+    return (_lib or _load()).csa2_paged_attend(
         cache.ref, batch, tq, _ptr(qpos, _I64, dev, (rows,)), _ptr(q, _BF16, dev, (rows, 64, 512)),
         _ptr(idx, _I32, dev, (rows, k)), k, _ptr(swa_begin, _I64, dev, (batch,)), win, ratio, sm_scale,
         _ptr(out, _BF16, dev, (rows, 64, 512)), _ptr(out_f32, _F32, dev, (rows, 64, 512)),
         _ptr(lse, _F32, dev, (rows, 64)), at, size, _stream(stream, dev))
-    if s:
-        raise Csa2Error("csa2_paged_attend", s)
 
 
 def csa2_paged_index_topk(cache: PagedCache, batch, tq, qpos, idx_q, k, out_idx, ws, ratio=1, max_ctx=None, flags=0,
