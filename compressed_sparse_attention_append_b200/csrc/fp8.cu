@@ -354,7 +354,9 @@ fp8_cols_kernel(Fp8GemmArgs a, const __grid_constant__ CUtensorMap wmap, const _
 // tensor cores write one, the other is read. The reading bounds it: without the products of the scales the
 // rest of the kernel takes 420 us where the whole takes 565 (4096 x 4096 x 32768, 1.95 PFLOP/s). Tried and
 // slower there: 16 reading warps (700 us), four accumulators of 128 columns (917), pairs of CTAs sharing
-// the weights (cta_group::2: 571, and 45 against 28 for 128 rows).
+// the weights (cta_group::2: 571, and 45 against 28 for 128 rows), the two column halves on barriers of their
+// own (710). Tiles of 224 columns would give 128 x 32768 all SMs, but a part of theirs has two scales: 38 us
+// against 29. Asking L2 for the first weights while the kernel before runs: no gain.
 // The tile leaves through shared memory, so that a warp's stores are whole lines of a row at any alignment.
 constexpr int kRowsThreads = 384;
 // registers at launch: 168 x 384; the copying warpgroup gives up 112, the two others take 56 each
