@@ -349,24 +349,31 @@ struct Token {
     int64_t rpos;         // its position for the rotation
     int64_t row;          // plane row (latent, key) or ring row (window)
 };
-// `first`: one lane of those that work on the token, which reports what is wrong with it
-__device__ __forceinline__ Token locate(const PagedAppendArgs& a, int kind, int64_t tok, int64_t tokens, bool first) {
+// Rows that a sequence may have of one kind: the ring keeps the latest swa_cap tokens (an older one of the call would
+// share its slot with a newer one), so no warp is started for the others.
+__host__ __device__ __forceinline__ int rows_of(const PagedAppendArgs& a, int kind) {
+    return kind == 2 && a.c.swa_cap < a.t ? (int)a.c.swa_cap : a.t;
+}
+// Row `id` of a kind. `first`: one lane of those that work on it, which reports what is wrong with it
+__device__ __forceinline__ Token locate(const PagedAppendArgs& a, int kind, int64_t id, bool first) {
     Token k{};
-    if (tok >= tokens) return k;
+    const int t = rows_of(a, kind);
+    const int64_t ids = (int64_t)a.batch * t;
+    if (id >= ids) return k;
     // (in 32 bits where they suffice: a 64-bit division costs a fifth of a row's arithmetic)
-    const int b = tokens <= 0x7FFFFFFF ? (int)((uint32_t)tok / (uint32_t)a.t) : (int)(tok / a.t);
-    const int i = (int)(tok - (int64_t)b * a.t);
-    const int64_t p0 = a.pos[b], p = p0 + i;
+    const int b = ids <= 0x7FFFFFFF ? (int)((uint32_t)id / (uint32_t)t) : (int)(id / t);
+    int i = (int)(id - (int64_t)b * t);
     const int n = a.len ? a.len[b] : a.t;
+    const int64_t p0 = a.pos[b];
     const int64_t cap = a.pg.max_pages << a.pg.shift;
     if (n < 0 || n > a.t || (n > 0 && (p0 < 0 || (kind < 2 && (p0 > cap || p0 + n > cap))))) {
         if (i == 0 && first) set_status(a.status, CSA2_DEV_BAD_POS);
         return k;
     }
+    if (n > t) i += n - t;
     if (i >= n) return k;  // padding
+    const int64_t p = p0 + i;
     if (kind == 2) {
-        // the ring keeps the latest swa_cap tokens: an older one of this call shares its slot with a newer one
-        if ((int64_t)i < (int64_t)n - a.c.swa_cap) return k;
         const int64_t slot = paged_slot(a.pg, b);
         k.live = slot >= 0;
         k.row = slot * a.c.swa_cap + (p & (a.c.swa_cap - 1));
@@ -377,7 +384,7 @@ __device__ __forceinline__ Token locate(const PagedAppendArgs& a, int kind, int6
     if (!k.live && first) set_status(a.status, CSA2_DEV_BAD_PAGE);
     const AppendRow& R = a.row[kind];
     k.src = R.x + (int64_t)b * R.x_batch + (int64_t)i * R.x_token;
-    k.rpos = a.rpos ? a.rpos[tok] : p;
+    k.rpos = a.rpos ? a.rpos[(int64_t)b * a.t + i] : p;
     return k;
 }
 
@@ -391,7 +398,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) paged_append_kernel(cons
     while (at + 1 < a.kinds && blockIdx.x >= a.first[at + 1]) ++at;
     const int kind = a.kind[at];
     const AppendRow& R = a.row[kind];
-    const int64_t wid = (int64_t)(blockIdx.x - a.first[at]) * kWarps + warp, tokens = (int64_t)a.batch * a.t;
+    const int64_t wid = (int64_t)(blockIdx.x - a.first[at]) * kWarps + warp;
     unsigned char* const mem = smem + (size_t)a.warp_bytes * warp;
     const WarpMem sm{mem, a.warp_bytes / 8};
     const float eps = (float)a.eps;
@@ -400,7 +407,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) paged_append_kernel(cons
     if (kind == 1) {
         // the keys of four tokens, 8 lanes each
         const int g = lane >> 3, gl = lane & 7, rot = (R.rot + 3) & ~3;
-        const Token k = locate(a, 1, wid * 4 + g, tokens, gl == 0);
+        const Token k = locate(a, 1, wid * 4 + g, gl == 0);
         if (!__any_sync(0xffffffffu, k.live)) return;
         bool sure = false;
         if (R.weight) {
@@ -424,7 +431,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) paged_append_kernel(cons
         }
         return;
     }
-    const Token k = locate(a, kind, wid, tokens, lane == 0);
+    const Token k = locate(a, kind, wid, lane == 0);
     if (!k.live) return;
     bool sure = false;
     if (R.weight) {
@@ -497,12 +504,11 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(PagedGatherArgs a) {
 }  // namespace
 
 cudaError_t launch_paged_append(PagedAppendArgs a, cudaStream_t s) {
-    const int64_t tokens = (int64_t)a.batch * a.t;
     int64_t blocks = 0;
     for (int i = 0; i < a.kinds; ++i) {
-        const int per = kWarps * (a.kind[i] == 1 ? 4 : 1);  // tokens of a block
+        const int per = kWarps * (a.kind[i] == 1 ? 4 : 1);  // rows of a block
         a.first[i] = (unsigned)blocks;
-        blocks += (tokens + per - 1) / per;
+        blocks += ((int64_t)a.batch * rows_of(a, a.kind[i]) + per - 1) / per;
         if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
         // 8 bytes per rotated channel of the rows that a warp holds
         const int rot = a.row[a.kind[i]].inv_freq ? (a.row[a.kind[i]].rot + 3) / 4 * 4 : 0;

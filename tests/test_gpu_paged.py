@@ -186,6 +186,32 @@ def test_append_of_padded_batches_strides_and_own_rotation_positions():
     assert int((c.l_data != 0).any(-1).sum()) == 24 + 7 + 1
 
 
+@pytest.mark.parametrize("normed", [False, True])
+def test_append_of_more_tokens_than_the_ring_holds(normed):
+    """Window rows only: the latest swa_cap of each sequence land, whatever its length; a bad length is reported once."""
+    B, t, cap = 7, 77, 16
+    main, _ = _ropes(False)
+    x = _rand(21, B, t, 512)
+    w = 1.0 + 0.1 * _rand(22, 512) if normed else None
+    pos = torch.tensor([0, 3, 1000, 15, 16, 2, 9], device=DEV)
+    ln = torch.tensor([77, 16, 17, 1, 0, 78, 31], dtype=torch.int32, device=DEV)
+    rpos = torch.randint(0, 1 << 20, (B, t), generator=_gen(23)).to(DEV)
+    for length, turned in ((ln, None), (ln, rpos), (None, None)):
+        c = _cache(B, 200, 8, swa_cap=cap)
+        c.swa.fill_(0x55)
+        ws = Status()
+        csa.csa2_paged_append(c, B, t, pos, swa=x, rope=main, w_swa=w, length=length, rpos=turned, eps=EPS, ws=ws)
+        assert ws.read() == (0 if length is None else csa.CSA2_DEV_BAD_POS)
+        for b in range(B):
+            n, p0 = t if length is None else int(ln[b]), int(pos[b])
+            want = torch.full((cap, 512), 0x55, dtype=torch.uint8)
+            if n <= t:
+                i = torch.arange(max(n - cap, 0), n)
+                at = (p0 + i) if turned is None else rpos[b, i.to(DEV)].cpu()
+                want[(p0 + i) % cap] = R.e4m3_rows(_want(x[b, i.to(DEV)], w, main, at))
+            assert torch.equal(c.swa[b].cpu(), want)
+
+
 def test_append_reports_and_skips_what_does_not_fit():
     B, t, page, pages = 6, 4, 8, 4
     c = _cache(B, pages, page, swa_slot=torch.tensor([0, 1, 2, 3, 9, 5], dtype=torch.int32, device=DEV))
