@@ -18,8 +18,9 @@
 //
 // Work split: 16 channels per lane (one scale block of the latent, half an MXFP4 block), so a warp takes one
 // latent or window row, or the indexer keys of four tokens. A row's rotated pairs are turned by its
-// lanes in turn, through shared memory. A row is a chain of loads and some 500 instructions, which bound it
-// (issue slots 76 % busy): 16 sequences of 2048 tokens at most, 853 on average, take 27 us.
+// lanes in turn, through shared memory. A row is a chain of loads and some 690 instructions (170 of them the
+// rotation's; a row of padding 106, the keys of four tokens 980), which bound it (issue slots 77 % busy): 16
+// sequences of 2048 tokens at most, 853 on average, take 24 us.
 #include "csa2_internal.cuh"
 #include "csa2_layer.cuh"
 
