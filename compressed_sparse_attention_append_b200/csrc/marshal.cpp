@@ -227,7 +227,7 @@ PyObject* gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const auto* wq = static_cast<const uint8_t*>(c.e4m3(a[2], {rows, k}));
         const auto* ws = static_cast<const float*>(c.dense(a[3], ScalarType::Float, {(rows + 127) / 128, nb}));
         void* to = c.strided(out, out->scalar_type(), {m, rows});
-        const int64_t stride = out->stride(0) > rows ? out->stride(0) : rows;
+        const int64_t stride = m > 1 ? out->stride(0) : rows;  // (a single row's means nothing; overlapping rows are refused)
         void* st = c.address(a[5]);
         const size_t bytes = (size_t)c.integer(a[6], 0, LLONG_MAX);
         void* s = c.stream(a[7]);

@@ -304,8 +304,8 @@ def _fp8_gemm(x, xs, w, ws, out, at, size, stream):
     assert o1 == 1 or n == 1, "expected dense rows"
     return (_lib or _load()).csa2_fp8_gemm(
         m, n, k, _ptr(x, _E4M3, dev, (m, k)), _ptr(xs, _F32, dev, (nb, m)), _ptr(w, _E4M3, dev, (n, k)),
-        _ptr(ws, _F32, dev, (-(-n // 128), nb)), _TYPES[dtype], _strided(out, dtype, dev, (m, n)), o0 if o0 > n else n, at,
-        size, _stream(stream, dev))
+        _ptr(ws, _F32, dev, (-(-n // 128), nb)), _TYPES[dtype], _strided(out, dtype, dev, (m, n)),
+        o0 if m > 1 else n, at, size, _stream(stream, dev))  # (a single row's stride means nothing)
 
 
 class PagedCache:

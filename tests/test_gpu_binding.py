@@ -1,0 +1,34 @@
+"""The binding of include/csa2_layer.h on the GPU: calls that it has to refuse, through the native marshalling and through
+the Python code alike. Everything here is refused on the host: no kernel runs on what is refused."""
+import pytest
+import torch
+
+import compressed_sparse_attention_append_b200 as csa
+from compressed_sparse_attention_append_b200 import layer
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(params=["native", "python"])
+def path(request, monkeypatch):
+    layer._load()
+    assert layer._fast is not None
+    if request.param == "python":
+        monkeypatch.setattr(layer, "_fast", None)
+    return request.param
+
+
+def test_a_product_into_overlapping_rows_is_refused(path):
+    m, n, k = 4, 8, 128
+    x, xs = torch.zeros(m, k, device=DEV, dtype=torch.uint8), torch.ones(1, m, device=DEV)
+    w, ws = torch.zeros(n, k, device=DEV, dtype=torch.uint8), torch.ones(1, 1, device=DEV)
+    for dtype in (torch.bfloat16, torch.float32):
+        store = torch.full((m * n,), 7.0, device=DEV, dtype=dtype)
+        for strides in ((0, 1), (1, 1), (7, 1)):
+            with pytest.raises(csa.Csa2Error) as e:
+                csa.csa2_fp8_gemm(x, xs, w, ws, store.as_strided((m, n), strides))
+            assert e.value.status == csa.CSA2_ERR_INVALID_ARG
+        assert bool((store == 7.0).all())
+        csa.csa2_fp8_gemm(x[:1], xs[:, :1].contiguous(), w, ws, store.as_strided((1, n), (3, 1)))  # a single row
+        assert not bool(store[:n].any()) and bool((store[n:] == 7.0).all())
