@@ -32,6 +32,12 @@ decltype(&csa2_paged_attend) f_attend;
 
 using c10::ScalarType;
 
+// layer.py's _rope_on
+struct RopeOn {
+    csa2_rope_spec spec;
+    int dev;
+};
+
 // The checks of one call; the first that fails leaves `ok` false.
 struct Call {
     bool ok = true;
@@ -96,6 +102,12 @@ struct Call {
         }
         return PyFloat_AS_DOUBLE(o);
     }
+    // None, or the address of a rotation, which has to be of the call's device
+    const csa2_rope_spec* rope(PyObject* o) {
+        const auto* r = static_cast<const RopeOn*>(address(o));
+        need(!r || (ok && r->dev == dev));
+        return ok && r ? &r->spec : nullptr;
+    }
     // None: the current stream; else a handle
     void* stream(PyObject* o) {
         if (o != Py_None) return address(o);
@@ -154,7 +166,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t t = x->size(0), d = x->size(2);
         csa2_heads h;
         heads(c, &h, a[2], a[3], Py_None, x->scalar_type(), t, d);
-        const auto* spec = static_cast<const csa2_rope_spec*>(c.address(a[0]));
+        const auto* spec = c.rope(a[0]);
         const auto* pos = static_cast<const int64_t*>(c.dense_or_none(a[1], ScalarType::Long, {t}));
         const int type = type_code(x->scalar_type());
         void* s = c.stream(a[4]);
@@ -178,7 +190,7 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         heads(c, &hq, a[3], a[5], a[4], q->scalar_type(), t, d);
         const bool keys = a[6] != Py_None;
         if (keys) heads(c, &hk, a[6], a[8], a[7], q->scalar_type(), t, d);
-        const auto* spec = static_cast<const csa2_rope_spec*>(c.address(a[0]));
+        const auto* spec = c.rope(a[0]);
         const auto* pos = static_cast<const int64_t*>(c.dense_or_none(a[1], ScalarType::Long, {t}));
         const int type = type_code(q->scalar_type());
         const float eps = (float)c.real(a[2]);
@@ -247,7 +259,7 @@ bool row(Call& c, csa2_append_row* r, PyObject* px, PyObject* pw, PyObject* spec
     r->x = static_cast<const uint16_t*>(c.strided(x, ScalarType::BFloat16, {batch, t, channels}));
     r->x_batch = x->stride(0), r->x_token = x->stride(1);
     r->weight = static_cast<const uint16_t*>(c.dense_or_none(pw, ScalarType::BFloat16, {channels}));
-    r->rope = static_cast<const csa2_rope_spec*>(c.address(spec));
+    r->rope = c.rope(spec);
     return true;
 }
 

@@ -60,6 +60,11 @@ class csa2_paged_cache(ctypes.Structure):
     _fields_ += [("page", ctypes.c_int)]
 
 
+class _rope_on(ctypes.Structure):
+    """A rotation and the device that its frequencies lie on, as csrc/marshal.cpp reads them."""
+    _fields_ = [("spec", csa2_rope_spec), ("dev", ctypes.c_int)]
+
+
 def declare(L):
     """The signatures of include/csa2_layer.h on the loaded library."""
     vp, i, i64, u32, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float, ctypes.c_size_t
@@ -175,16 +180,22 @@ def _status(ws):
 
 class Rope:
     """A rotation (csa2_rope_spec) and the tensor of its frequencies: inv_freq [rot / 2] float64, radians
-    per position; `offset` the first rotated channel; `inverse` turns back."""
+    per position, on the device that it is used on; `offset` the first rotated channel; `inverse` turns back."""
 
     def __init__(self, inv_freq, offset=0, interleaved=False, mscale=1.0, inverse=False):
         self.inv_freq, self.offset, self.interleaved = inv_freq, int(offset), bool(interleaved)
         self.mscale, self.inverse = float(mscale), bool(inverse)
         self.rot = 2 * inv_freq.numel()
-        self.c = csa2_rope_spec(_ptr(inv_freq, _F64, _device(), (self.rot // 2,)), self.rot, self.offset, int(self.interleaved),
-                                int(self.inverse), self.mscale)
-        self.ref = ctypes.pointer(self.c)
+        dev = _device()
+        self.c = _rope_on((_ptr(inv_freq, _F64, dev, (self.rot // 2,)), self.rot, self.offset, int(self.interleaved),
+                           int(self.inverse), self.mscale), dev)
+        self.ref = ctypes.pointer(self.c.spec)
         self.at = ctypes.addressof(self.c)
+
+    def on(self, dev):
+        """Itself, for a call on device `dev`."""
+        assert self.c.dev == dev, "expected a rotation of the current device"
+        return self
 
     @classmethod
     def for_context(cls, rot, base=10000.0, scaling="plain", factor=1.0, orig_ctx=0, beta_fast=32.0, beta_slow=1.0,
@@ -233,7 +244,7 @@ def _rope(rope, pos, x, out, stream):
     assert dtype in _TYPES, "expected a bf16 or fp32 tensor"
     h = _heads(x, out, None, dtype, dev, tokens, d)
     return (_lib or _load()).csa2_rope(
-        rope.ref, _TYPES[dtype], tokens, d, _ptr(pos, _I64, dev, (tokens,)), h, _stream(stream, dev))
+        rope.on(dev).ref, _TYPES[dtype], tokens, d, _ptr(pos, _I64, dev, (tokens,)), h, _stream(stream, dev))
 
 
 def csa2_norm_rope(rope, pos, eps, q, wq, q_out, k=None, wk=None, k_out=None, stream=None):
@@ -253,7 +264,7 @@ def _norm_rope(rope, pos, eps, q, wq, q_out, k, wk, k_out, stream):
     hq = _heads(q, q_out, wq, dtype, dev, tokens, d)
     hk = None if k is None else _heads(k, k_out, wk, dtype, dev, tokens, d)
     return (_lib or _load()).csa2_norm_rope(
-        None if rope is None else rope.ref, _TYPES[dtype], tokens, d, _ptr(pos, _I64, dev, (tokens,)), eps, hq, hk,
+        None if rope is None else rope.on(dev).ref, _TYPES[dtype], tokens, d, _ptr(pos, _I64, dev, (tokens,)), eps, hq, hk,
         _stream(stream, dev))
 
 
@@ -352,7 +363,7 @@ def _append_row(x, weight, rope, dev, batch, t, channels):
     x0, x1, x2 = x.stride()
     assert x2 == 1, f"expected dense rows [{batch}, {t}, {channels}]"
     return _row_bytes(_strided(x, _BF16, dev, (batch, t, channels)), x0, x1,
-                      0 if weight is None else _ptr(weight, _BF16, dev, (channels,)), 0 if rope is None else rope.at)
+                      0 if weight is None else _ptr(weight, _BF16, dev, (channels,)), 0 if rope is None else rope.on(dev).at)
 
 
 def csa2_paged_append(cache: PagedCache, batch, t, pos, latent=None, idx_k=None, swa=None, rope=None, idx_rope=None,

@@ -32,3 +32,22 @@ def test_a_product_into_overlapping_rows_is_refused(path):
         assert bool((store == 7.0).all())
         csa.csa2_fp8_gemm(x[:1], xs[:, :1].contiguous(), w, ws, store.as_strided((1, n), (3, 1)))  # a single row
         assert not bool(store[:n].any()) and bool((store[n:] == 7.0).all())
+
+
+def test_rotations_of_another_device_are_refused(path):
+    """(They are this device's and only say that they are another's: nothing foreign is ever reached.)"""
+    own, far = (csa.Rope(torch.ones(8, device=DEV, dtype=torch.float64)) for _ in range(2))
+    far.c.dev = torch.cuda.current_device() + 1
+    x, pos = torch.ones(3, 2, 16, device=DEV), torch.arange(3, device=DEV)
+    cache = csa.PagedCache(2, 64, 1, 2)
+    cache.table.copy_(torch.arange(2, dtype=torch.int32, device=DEV))
+    row = torch.ones(1, 1, 512, device=DEV, dtype=torch.bfloat16)
+    for call in (lambda r: csa.csa2_rope(r, pos, x, x), lambda r: csa.csa2_norm_rope(r, pos, 1e-6, x, None, x),
+                 lambda r: csa.csa2_paged_append(cache, 1, 1, pos[:1], row, rope=r),
+                 lambda r: csa.csa2_paged_append(cache, 1, 1, pos[:1], swa=row, rope=own, swa_rope=r)):
+        call(own)
+        torch.cuda.synchronize()
+        before = [t.clone() for t in (x, cache.l_data, cache.swa)]
+        with pytest.raises(AssertionError, match="rotation of the current device"):
+            call(far)
+        assert all(torch.equal(a, b) for a, b in zip(before, (x, cache.l_data, cache.swa)))

@@ -58,3 +58,42 @@ def test_a_product_into_overlapping_rows_is_refused(host, monkeypatch, m, n, out
     with pytest.raises(csa.Csa2Error) as e:
         csa.csa2_fp8_gemm(*_product(m, n), out(), stream=0)
     assert e.value.status == INVALID
+
+
+class Foreign(torch.Tensor):
+    """A host tensor that says it lies on device 1."""
+
+    def get_device(self):
+        return 1
+
+
+def _on_device_1(monkeypatch, make):
+    with monkeypatch.context() as m:
+        m.setattr(layer, "_device", lambda: 1)
+        return make()
+
+
+def test_a_rotation_of_another_device_is_refused(host, monkeypatch):
+    rope = lambda: csa.Rope(torch.ones(8, dtype=torch.float64).as_subclass(Foreign))
+    far = _on_device_1(monkeypatch, rope)
+    x, pos = torch.zeros(3, 2, 16), torch.zeros(3, dtype=torch.int64)
+    own = csa.Rope(torch.ones(8, dtype=torch.float64))
+    cache = csa.PagedCache(2, 64, 1, 2, device="cpu")
+    row = torch.zeros(1, 1, 512, dtype=torch.bfloat16)
+    key = torch.zeros(1, 1, 128, dtype=torch.bfloat16)
+    calls = [
+        lambda r: csa.csa2_rope(r, pos, x, x, stream=0),
+        lambda r: csa.csa2_norm_rope(r, pos, 1e-6, x, None, x, stream=0),
+        lambda r: csa.csa2_paged_append(cache, 1, 1, pos[:1], row, rope=r, stream=0),
+        lambda r: csa.csa2_paged_append(cache, 1, 1, pos[:1], None, key, idx_rope=r, stream=0),
+        lambda r: csa.csa2_paged_append(cache, 1, 1, pos[:1], swa=row, swa_rope=r, stream=0),
+    ]
+    for call in calls:
+        call(own)
+        assert len(host.calls) == 1
+        with pytest.raises(AssertionError, match="rotation of the current device"):
+            call(far)
+        with pytest.raises(AssertionError, match="rotation of the current device"):
+            call(_on_device_1(monkeypatch, far.transposed))
+        assert len(host.calls) == 1
+        host.calls.clear()
