@@ -175,7 +175,12 @@ def _load():
 
 
 def _status(ws):
-    return (None, 0) if ws is None else (ws.ptr, ws.nbytes)
+    """Address and size of a workspace, which has to be the current device's."""
+    if ws is None:
+        return None, 0
+    buf = getattr(ws, "buf", None)
+    assert buf is None or buf.get_device() == _device(), "expected a workspace of the current device"
+    return ws.ptr, ws.nbytes
 
 
 class Rope:

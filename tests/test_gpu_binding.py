@@ -34,7 +34,7 @@ def test_a_product_into_overlapping_rows_is_refused(path):
         assert not bool(store[:n].any()) and bool((store[n:] == 7.0).all())
 
 
-def test_rotations_of_another_device_are_refused(path):
+def test_rotations_and_workspaces_of_another_device_are_refused(path):
     """(They are this device's and only say that they are another's: nothing foreign is ever reached.)"""
     own, far = (csa.Rope(torch.ones(8, device=DEV, dtype=torch.float64)) for _ in range(2))
     far.c.dev = torch.cuda.current_device() + 1
@@ -51,3 +51,18 @@ def test_rotations_of_another_device_are_refused(path):
         with pytest.raises(AssertionError, match="rotation of the current device"):
             call(far)
         assert all(torch.equal(a, b) for a, b in zip(before, (x, cache.l_data, cache.swa)))
+
+    class Ws:
+        nbytes = 256
+
+        def __init__(self, buf):
+            self.buf, self.ptr = buf, buf.data_ptr()
+
+    class Foreign(torch.Tensor):
+        def get_device(self):
+            return torch.cuda.current_device() + 1
+
+    buf = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    csa.csa2_paged_append(cache, 1, 1, pos[:1], row, ws=Ws(buf))
+    with pytest.raises(AssertionError, match="workspace of the current device"):
+        csa.csa2_paged_append(cache, 1, 1, pos[:1], row, ws=Ws(buf.as_subclass(Foreign)))

@@ -97,3 +97,32 @@ def test_a_rotation_of_another_device_is_refused(host, monkeypatch):
             call(_on_device_1(monkeypatch, far.transposed))
         assert len(host.calls) == 1
         host.calls.clear()
+
+
+class Ws:
+    nbytes = 1 << 20
+
+    def __init__(self, buf):
+        self.buf, self.ptr = buf, buf.data_ptr()
+
+
+def test_a_workspace_of_another_device_is_refused(host):
+    buf = torch.zeros(256, dtype=torch.uint8)
+    own, far = Ws(buf), Ws(buf.as_subclass(Foreign))
+    cache = csa.PagedCache(2, 64, 1, 2, device="cpu")
+    pos, idx = torch.zeros(1, dtype=torch.int64), torch.zeros(1, 4, dtype=torch.int32)
+    q, out = torch.zeros(1, 64, 512, dtype=torch.bfloat16), torch.zeros(1, 64, 512, dtype=torch.bfloat16)
+    calls = [
+        lambda ws: csa.csa2_fp8_gemm(*_product(4, 8), torch.empty(4, 8), status=ws, stream=0),
+        lambda ws: csa.csa2_paged_append(cache, 1, 1, pos, q[:, :1, :], ws=ws, stream=0),
+        lambda ws: csa.csa2_paged_gather(cache, 1, idx, torch.zeros(1, 4, 512, dtype=torch.bfloat16), ws=ws, stream=0),
+        lambda ws: csa.csa2_paged_attend(cache, 1, 1, pos, q, idx, 4, out, ws=ws, stream=0),
+        lambda ws: csa.csa2_paged_index_topk(cache, 1, 1, pos, q[:, :4, :128].contiguous(), 4, idx, ws, stream=0),
+    ]
+    for call in calls:
+        call(own)
+        assert len(host.calls) == 1 and own.ptr in host.calls[0][1]
+        with pytest.raises(AssertionError, match="workspace of the current device"):
+            call(far)
+        assert len(host.calls) == 1
+        host.calls.clear()
