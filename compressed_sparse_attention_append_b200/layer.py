@@ -183,7 +183,16 @@ def _status(ws):
     return ws.ptr, ws.nbytes
 
 
-class Rope:
+class _Fixed:
+    """The attributes that a C struct was made from are set once: the struct would not follow them."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"{name} is fixed: fill its tensor in place, or make another {type(self).__name__}")
+        super().__setattr__(name, value)
+
+
+class Rope(_Fixed):
     """A rotation (csa2_rope_spec) and the tensor of its frequencies: inv_freq [rot / 2] float64, radians
     per position, on the device that it is used on; `offset` the first rotated channel; `inverse` turns back."""
 
@@ -324,9 +333,9 @@ def _fp8_gemm(x, xs, w, ws, out, at, size, stream):
         o0 if m > 1 else n, at, size, _stream(stream, dev))  # (a single row's stride means nothing)
 
 
-class PagedCache:
+class PagedCache(_Fixed):
     """Planes of csa2_paged_cache, allocated with torch unless given: n_pages pages of `page` entries, the page
-    table of `batch` sequences ([batch, max_pages] int32, -1 = no page; the caller fills `table`) and
+    table of `batch` sequences ([batch, max_pages] int32, -1 = no page; the caller fills `table` in place) and
     n_slots window rings (default: one per sequence; swa_slot [batch] int32 names each sequence's)."""
 
     def __init__(self, n_pages, page, batch, max_pages, swa_cap=128, n_slots=None, swa_slot=None, device="cuda",

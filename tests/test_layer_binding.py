@@ -126,3 +126,16 @@ def test_a_workspace_of_another_device_is_refused(host):
             call(far)
         assert len(host.calls) == 1
         host.calls.clear()
+
+
+def test_what_a_struct_was_made_from_cannot_be_replaced(host):
+    """A new tensor in its place would not reach the library, which keeps the old one's address."""
+    cache = csa.PagedCache(2, 64, 1, 2, device="cpu", swa_slot=torch.zeros(1, dtype=torch.int32))
+    rope = csa.Rope(torch.ones(8, dtype=torch.float64), offset=2, mscale=1.5)
+    for what in (cache, rope):
+        for name, value in list(vars(what).items()):
+            with pytest.raises(AttributeError, match="fixed"):
+                setattr(what, name, value)
+    cache.table[0, 1] = 1  # in place it is the caller's
+    assert cache.table.data_ptr() == cache.c.table and cache.swa_slot.data_ptr() == cache.c.swa_slot
+    assert rope.inv_freq.data_ptr() == rope.c.spec.inv_freq
