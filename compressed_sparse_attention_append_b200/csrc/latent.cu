@@ -42,7 +42,8 @@
 // scales are read once, 8 a lane, and passed between its lanes. The row's indices are checked
 // and staged in shared memory once, so no tile waits on a dependent index load. Q arrives by one bulk copy.
 // Tensor memory: S^T in columns 0..63, O^T in columns 64..319 (channels on the lanes).
-// The result is normalised by the per-head sum of P at the end: out = O / l, lse = m ln 2 + ln l.
+// The result is normalised by the per-head sum of P at the end: out = O / l, lse = m ln 2 + ln l. A row without a
+// key has l = 0 exactly; with one, l is about 1 or more, or NaN (a logit that is not finite), which goes into out and lse.
 // Every wait on the tensor cores is bounded; one that runs out sets CSA2_DEV_TIMEOUT.
 #include "csa2_internal.cuh"
 #include "tc.cuh"
@@ -495,10 +496,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_kernel(LatentAttend
             for (int r = 0; r < split; ++r) m = fmaxf(m, ld_cluster(smem_u32(&s_m[tid]), r));
             for (int r = 0; r < split; ++r) {
                 const float mr = ld_cluster(smem_u32(&s_m[tid]), r), lr = ld_cluster(smem_u32(&s_l[tid]), r);
-                if (mr != -INFINITY) l = fmaf(lr, exp2f(mr - m), l);
+                if (lr != 0.f) l = fmaf(lr, exp2f(mr - m), l);
             }
-            const bool em = m == -INFINITY || !(l > 0.f);
-            s_al[tid] = em || s_m[tid] == -INFINITY ? 0.f : exp2f(s_m[tid] - m) / l;
+            const bool em = l == 0.f;
+            s_al[tid] = s_l[tid] == 0.f ? 0.f : exp2f(s_m[tid] - m) / l;
             if (a.lse && rank == 0) a.lse[(size_t)row * kLatHQ + tid] = em ? -INFINITY : m * 0.6931471805599453f + logf(l);
         }
         __syncthreads();
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_kernel(LatentAttend
     if (tid < 64) {
         const float l = (red[tid] + red[64 + tid]) + (red[128 + tid] + red[192 + tid]);
         s_l[tid] = l;
-        const bool em = (nt == 0) || (s_m[tid] == -INFINITY) || !(l > 0.f);
+        const bool em = nt == 0 || l == 0.f;
         s_al[tid] = em ? 0.f : 1.f / l;  // 1 / l per head (0 for a row with no key: O is 0 there)
     }
     __syncthreads();
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_kernel(LatentAttend
         }
     }
     if (a.lse && tid < 64) {
-        const bool e = (nt == 0) || (s_m[tid] == -INFINITY) || !(s_l[tid] > 0.f);
+        const bool e = nt == 0 || s_l[tid] == 0.f;
         a.lse[(size_t)row * kLatHQ + tid] = e ? -INFINITY : (s_m[tid] * 0.6931471805599453f + logf(s_l[tid]));
     }
     tc_fence_before();
