@@ -13,14 +13,15 @@
 //     whose bf16 values lie on borders often, are always formed so.
 // The error of fp32: the sum of squares is off by 4 roundings (a lane's 16 as a tree, the lanes' sums in 64 bits),
 // its root by half of that and 2^-23.4, the product by 2^-24, the quotient by 2^-23 more: below 2^-21.3. Cosine
-// and sine are off by 2^-21.4. So e = 2^-21 |y|, and 2^-20 m (|a| + |b|) for the channels of a rotated pair
-// (a, b), cover y and its quotient.
+// and sine are off by 2^-21.4 at any position below 2^31 (angle.cuh). So e = 2^-21 |y|, and 2^-20 m (|a| + |b|) for
+// the channels of a rotated pair (a, b), cover y and its quotient.
 //
 // Work split: 16 channels per lane (one scale block of the latent, half an MXFP4 block), so a warp takes one
 // latent or window row, or the indexer keys of four tokens. A row's rotated pairs are turned by its
 // lanes in turn, through shared memory. A row is a chain of loads and some 690 instructions (170 of them the
 // rotation's; a row of padding 106, the keys of four tokens 980), which bound it (issue slots 77 % busy): 16
 // sequences of 2048 tokens at most, 853 on average, take 24 us.
+#include "angle.cuh"
 #include "csa2_internal.cuh"
 #include "csa2_layer.cuh"
 
@@ -30,7 +31,6 @@ namespace {
 
 constexpr int kWarps = 4;    // per block
 constexpr int kBlocks = 10;  // per SM (registers): a row is a chain of loads, so many rows at once
-constexpr double kInvPi = 0.31830988618379067154;
 
 // Rounding to odd: the fp32 value next to v towards zero, its last bit set unless it is v. A further
 // rounding to a format of at most 22 bits then decides as it would for v.
@@ -60,11 +60,6 @@ __device__ __forceinline__ void load_row(const uint16_t* src, int lane, float (&
         x[2] = __uint_as_float(v.y << 16);
         x[3] = __uint_as_float(v.y & 0xFFFF0000u);
     }
-}
-// half turns of pos * f, in [-1, 1]
-__device__ __forceinline__ double half_turns(int64_t pos, double f) {
-    const double h = ((double)pos * f) * kInvPi;
-    return h - 2.0 * rint(0.5 * h);
 }
 // the channels of pair j within the rotated range
 __device__ __forceinline__ int2 pair_of(const AppendRow& R, int j) {

@@ -2,8 +2,9 @@
 //
 // y = R_pos(x * w / sqrt(mean(x^2) + eps)): pair j of the rotated channels turns by t = pos * f_j,
 //   (a, b) -> m (a cos t - b sin t, b cos t + a sin t).
-// The angle is a 64-bit product (a far position times a frequency loses whole radians in 32 bits),
-// reduced to half turns in 64 bits and handed to sincospif, whose argument then lies in [-1, 1].
+// The angle (a far position times a frequency loses whole radians in 32 bits) is formed and reduced to half
+// turns in 64 bits, their rounding errors carried along (angle.cuh), and handed to sincospif, whose argument
+// then lies in [-1, 1].
 // Everything else is fp32, rounded once when it is stored.
 //
 // Both calls move each row once and compute little, so device memory bounds them. Split: a block
@@ -13,6 +14,7 @@
 // block run on from one token to the next, so no head count leaves a block half empty. With
 // CSA2_ROPE_HALF a lane takes vectors in pairs, rot / 2 channels apart where they turn, so that both
 // channels of every rotated pair are its own.
+#include "angle.cuh"
 #include "csa2_internal.cuh"
 #include "csa2_layer.cuh"
 
@@ -21,14 +23,11 @@ namespace csa2 {
 namespace {
 
 constexpr int kThr = 256;
-constexpr double kInvPi = 0.31830988618379067154;
 
 // cos and sin of pos * f (radians)
 __device__ __forceinline__ float2 turn(int64_t pos, double f, float mscale, int transposed) {
-    double h = ((double)pos * f) * kInvPi;  // half turns
-    h -= 2.0 * rint(0.5 * h);
     float s, c;
-    sincospif((float)h, &s, &c);
+    sincospif((float)half_turns(pos, f), &s, &c);
     return make_float2(c * mscale, (transposed ? -s : s) * mscale);
 }
 
@@ -96,12 +95,13 @@ struct Turns {
 
 // One row per group of a.lanes lanes, CPL vectors per lane; ITER rows of a group are in flight, and with a
 // norm a group takes a.rounds * ITER rows in turn. Measured for 4096 tokens x 64 heads x 512, bf16: the
-// rotation alone is fastest with four rows in flight and one round (83 us, 6.4 TB/s; two rows 88); the norm, whose
-// instructions weigh as much as its bytes, with one row, eight rounds and five blocks an SM (99 us,
+// rotation alone is fastest with four rows in flight, three blocks an SM and one round (83 us, 6.4 TB/s; two rows 88,
+// two blocks an SM 99); the norm, whose instructions
+// weigh as much as its bytes, with one row, eight rounds and five blocks an SM (99 us,
 // 5.5 TB/s; one round 108, two rows 118). Rows of 128 channels: 16384 tokens x 33 heads 81 us (3.4 TB/s), in
 // halves over the whole head 16384 x 20 heads 46 us (3.7 TB/s): shorter rows, more instructions per byte.
 template <typename T, int VB, int CPL, int ITER, bool NORM, bool HALF>
-__global__ void __launch_bounds__(kThr, NORM && CPL <= 2 ? (HALF ? 4 : 5) : 1) rotate_kernel(RotateArgs a) {
+__global__ void __launch_bounds__(kThr, NORM && CPL <= 2 ? (HALF ? 4 : 5) : ITER == 4 && CPL == 2 ? 3 : 1) rotate_kernel(RotateArgs a) {
     constexpr int E = VB / (int)sizeof(T);
     using V = Vec<VB>;
     extern __shared__ __align__(16) float table[];  // [tokens of the block][rot / 2] cosines, then the sines

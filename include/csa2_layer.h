@@ -45,8 +45,8 @@ extern "C" {
  * t = position * inv_freq[j],
  *     (a, b) -> mscale * (a cos t - b sin t, b cos t + a sin t);
  * the other channels stay as they are. With `transposed` the sine changes its sign: the rotation back
- * (and, with mscale, the transposed matrix, which is its gradient). Angles are formed in 64 bits, so
- * they hold at any position below 2^31.
+ * (and, with mscale, the transposed matrix, which is its gradient). Angles are reduced in 64 bits with
+ * their rounding errors carried along, so they hold to 64-bit accuracy at any position below 2^31.
  */
 typedef struct {
     const double* inv_freq; /* device [rot / 2]: radians per position, 8-byte aligned */
