@@ -16,7 +16,7 @@ One decode step of a layer of the pages' own shape, `B` sequences (bf16 unless n
                       w_latent=w_l, w_idx_k=w_k, w_swa=w_s, eps=eps, ws=ws)
     csa2_paged_index_topk(cache, B, 1, pos, idx_q, 512, idx, index_ws)
     csa2_paged_attend(cache, B, 1, pos, q, idx, 512, out, ws=ws)
-    csa2_rope(rope.transposed(), pos, out, out)            # K = V: the output turned back
+    csa2_rope(rope.inverted(), pos, out, out)              # K = V: the output turned back, mscale taken out
 """
 from __future__ import annotations
 
@@ -194,7 +194,8 @@ class _Fixed:
 
 class Rope(_Fixed):
     """A rotation (csa2_rope_spec) and the tensor of its frequencies: inv_freq [rot / 2] float64, radians
-    per position, on the device that it is used on; `offset` the first rotated channel; `inverse` turns back."""
+    per position, on the device that it is used on; `offset` the first rotated channel; `inverse` turns the other way
+    (times mscale as well)."""
 
     def __init__(self, inv_freq, offset=0, interleaved=False, mscale=1.0, inverse=False):
         self.inv_freq, self.offset, self.interleaved = inv_freq, int(offset), bool(interleaved)
@@ -219,8 +220,14 @@ class Rope(_Fixed):
         return cls(f.to(device), offset, interleaved, mscale)
 
     def transposed(self):
-        """The rotation back (times mscale again: the transposed matrix)."""
+        """The transposed matrix (turned back, times mscale again): the rotation's gradient."""
         return Rope(self.inv_freq, self.offset, self.interleaved, self.mscale, not self.inverse)
+
+    def inverted(self):
+        """The inverse (turned back, divided by mscale): what undoes the rotation. With K = V the attention's output
+        needs it. (A rotation made with mscale 1 keeps the scale out of the values; mscale^2 / sqrt(512) is then
+        the sm_scale of a head that is rotated whole.)"""
+        return Rope(self.inv_freq, self.offset, self.interleaved, 1.0 / (self.mscale or 1.0), not self.inverse)
 
 
 def csa2_rope_frequencies(rot, base=10000.0, scaling="plain", factor=1.0, orig_ctx=0, beta_fast=32.0, beta_slow=1.0):

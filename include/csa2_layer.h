@@ -14,7 +14,7 @@
  *   csa2_paged_append                     latent, indexer key, window row: norm, rotation, codec, write
  *   csa2_paged_index_topk                 the selection
  *   csa2_paged_attend                     attention over selected entries and the window
- *   csa2_rope (transposed)                the output turned back (K = V carries the keys' rotation)
+ *   csa2_rope (transposed, 1 / mscale)    the output turned back (K = V carries the keys' rotation and scale)
  *   csa2_fp8_quantize, csa2_fp8_gemm      output projection
  */
 #ifndef CSA2_LAYER_H
@@ -44,9 +44,10 @@ extern "C" {
  * A rotation: pair j of the channels offset .. offset + rot - 1 of a head turns by the angle
  * t = position * inv_freq[j],
  *     (a, b) -> mscale * (a cos t - b sin t, b cos t + a sin t);
- * the other channels stay as they are. With `transposed` the sine changes its sign: the rotation back
- * (and, with mscale, the transposed matrix, which is its gradient). Angles are reduced in 64 bits with
- * their rounding errors carried along, so they hold to 64-bit accuracy at any position below 2^31.
+ * the other channels stay as they are. With `transposed` the sine changes its sign: with the same
+ * mscale that is the transposed matrix, the gradient; with 1 / mscale it is the inverse, which undoes
+ * the rotation. Angles are reduced in 64 bits with their rounding errors carried along, so they hold to
+ * 64-bit accuracy at any position below 2^31.
  */
 typedef struct {
     const double* inv_freq; /* device [rot / 2]: radians per position, 8-byte aligned */

@@ -139,3 +139,15 @@ def test_what_a_struct_was_made_from_cannot_be_replaced(host):
     cache.table[0, 1] = 1  # in place it is the caller's
     assert cache.table.data_ptr() == cache.c.table and cache.swa_slot.data_ptr() == cache.c.swa_slot
     assert rope.inv_freq.data_ptr() == rope.c.spec.inv_freq
+
+
+def test_the_inverse_of_a_rotation_takes_its_scale_out(host):
+    f = torch.ones(8, dtype=torch.float64)
+    for mscale in (1.0, 1.277, 0.5, 0.0):  # (0 stands for 1)
+        rope = csa.Rope(f, offset=2, interleaved=True, mscale=mscale)
+        back, again, t = rope.inverted(), rope.inverted().inverted(), rope.transposed()
+        m = mscale or 1.0
+        for r, scale, turned in ((back, 1.0 / m, 1), (again, m, 0), (t, mscale, 1)):
+            s = r.c.spec
+            assert (s.inv_freq, s.rot, s.offset, s.layout, s.transposed) == (f.data_ptr(), 16, 2, 1, turned)
+            assert abs(s.mscale - scale) <= 2.0 ** -23 * scale
