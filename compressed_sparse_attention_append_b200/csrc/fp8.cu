@@ -326,7 +326,6 @@ fp8_cols_kernel(Fp8GemmArgs a, const __grid_constant__ CUtensorMap wmap, const _
         }
     }
     if (split > 1) {
-        __syncwarp();
         cluster_sync();
         const int i0 = NT * rank / split, i1 = NT * (rank + 1) / split;
         for (int e = tid + i0 * 128; e < i1 * 128; e += G::kThreads) {

@@ -138,8 +138,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---- clusters --------------------------------------------------------------------------------------
-// Every thread of every CTA of the cluster, warps converged; orders shared-memory accesses across it.
+// Every thread of every CTA of the cluster; orders shared-memory accesses across it. (The aligned form wants each
+// warp converged, which a loop whose lanes leave it apart does not promise.)
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
