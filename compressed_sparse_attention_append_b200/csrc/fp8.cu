@@ -11,6 +11,7 @@
 
 #include "csa2_internal.cuh"
 #include "csa2_layer.cuh"
+#include "fp8_plan.h"
 #include "tc.cuh"
 
 namespace csa2 {
@@ -596,14 +597,6 @@ cudaError_t make_map(CUtensorMap* map, const uint8_t* p, int64_t rows, int k, in
                ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// The contraction split (by 2, 4 or 8), two blocks each at least: to about one CTA an SM, and up to two in
-// clusters of 4 at most (64 tiles of 32 blocks: 14.5 us by 2, 12.6 by 4; 32 tiles: 7.5 us by 4, 8.2 by 8).
-int cols_split(int64_t tiles, int nb) {
-    int split = 1;
-    while (split < 8 && nb >= split * 4 && tiles * split * 2 <= (split < 4 ? 296 : 160)) split *= 2;
-    return split;
-}
-
 template <int NT>
 cudaError_t launch_cols(const Fp8GemmArgs& a, cudaStream_t s) {
     using G = Cols<NT>;
@@ -615,7 +608,7 @@ cudaError_t launch_cols(const Fp8GemmArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int64_t tiles = ((a.n + 127) / 128) * ((a.m + NT - 1) / NT);
     const int nb = (a.k + 127) / 128;
-    const int split = cols_split(tiles, nb);
+    const int split = fp8_cols_split(tiles, nb);
     if (tiles * split > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     return launch_cluster(k, dim3((unsigned)(tiles * split)), dim3(G::kThreads), split, G::kSmem, s, a, wmap, xmap, split);
 }
@@ -662,15 +655,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t s) {
     if (a.m <= 16) return launch_cols<16>(a, s);
     if (a.m <= 32) return launch_cols<32>(a, s);
     if (a.m <= 64) return launch_cols<64>(a, s);
-    // Both kernels' time goes by the blocks that a CTA takes one after the other: 0.53 us a block with rows of x
-    // along the columns (two CTAs an SM, 64 rows each, the contraction split for few tiles), 0.57 us with
-    // them on the lanes (one CTA an SM, 128 rows x 256). Measured (us, columns / lanes): 128 x 2112 x 7168
-    // 13.7 / 34, 256 x 4096 x 4096 17.8 / 20, 777 x 4099 x 4112 47 / 26, 128 x 32768 x 4096 44 / 28.
-    const int nb = (a.k + 127) / 128;
-    const int64_t tc = ((a.n + 127) / 128) * ((a.m + 63) / 64), tr = ((a.n + 255) / 256) * ((a.m + 127) / 128);
-    const int split = cols_split(tc, nb);
-    const int64_t cols = (tc * split + 295) / 296 * ((nb + split - 1) / split), rows = (tr + 147) / 148 * nb;
-    return cols * 53 <= rows * 57 ? launch_cols<64>(a, s) : launch_rows_gemm(a, s);
+    return fp8_by_columns(a.m, a.n, a.k) ? launch_cols<64>(a, s) : launch_rows_gemm(a, s);
 }
 
 }  // namespace csa2
