@@ -139,6 +139,9 @@ CSA2_API csa2_status csa2_fp8_quantize_weight(int64_t n, int k, const uint16_t* 
  *   out [m][n], row i at out + i * out_stride (elements), bf16 or fp32 by out_dtype
  * Tensor cores (E4M3 products are exact, a block's sum is kept in fp32), the blocks' sums scaled and
  * added in fp32, one rounding to bf16. The result of a row does not depend on timing.
+ * The two scales of a block are multiplied with each other before they meet its sum: where xs * ws
+ * leaves fp32's normal range (2^-126 .. 2^128; operands of extreme sizes on both sides), the block loses
+ * bits, vanishes or is not finite even where its share of the result could be held.
  * k a positive multiple of 16, x and w 16-byte aligned, out aligned to its elements, out_stride >= n.
  * m and n any size >= 0, below 2^31. status: at least 256 bytes from csa2_workspace_init (its status
  * word receives CSA2_DEV_TIMEOUT if a tensor-core wait ran out), or NULL.

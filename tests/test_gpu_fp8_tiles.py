@@ -115,3 +115,16 @@ def test_joins_of_few_tiles_that_end_inside(m, n, k, dtype):
     _check(out, *ops)
     out.fill_(7.0)
     assert bool((frame == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,n,k", [(40, 300, 512), (2100, 6001, 656)])
+@pytest.mark.parametrize("up", [1.0, -1.0])
+def test_scales_of_opposite_extremes(m, n, k, dtype, up):
+    """Scales far outside each other's size whose product is an ordinary number (powers of two: the same result but for
+    them, bit for bit)."""
+    xq, xs, wq, ws = _operands(m, n, k)
+    want, out = torch.empty(m, n, device=DEV, dtype=dtype), torch.empty(m, n, device=DEV, dtype=dtype)
+    csa.csa2_fp8_gemm(xq, xs, wq, ws, want)
+    csa.csa2_fp8_gemm(xq, xs * 2.0 ** (100 * up), wq, ws * 2.0 ** (-100 * up), out)
+    assert torch.equal(out, want)
