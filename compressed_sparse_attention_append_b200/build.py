@@ -12,6 +12,7 @@ SRC = [os.path.join(HERE, "csrc", f) for f in ("abi.cu", "append.cu", "index.cu"
                                          "rope.cu", "fp8.cu", "paged.cu", "layer_abi.cu")]
 HDRS = [os.path.join(HERE, "csrc", "csa2_internal.cuh"), os.path.join(HERE, "csrc", "tc.cuh"), os.path.join(HERE, "csrc", "csa2_layer.cuh"),
         os.path.join(HERE, "csrc", "angle.cuh"), os.path.join(HERE, "csrc", "fp8_plan.h"),
+        os.path.join(HERE, "csrc", "attend_plan.h"),
         os.path.join(ROOT, "include", "csa2.h"), os.path.join(ROOT, "include", "csa2_layer.h")]
 LIB = os.path.join(HERE, "libcsa2.so")
 MARSHAL_SRC = os.path.join(HERE, "csrc", "marshal.cpp")

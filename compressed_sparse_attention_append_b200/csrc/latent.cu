@@ -45,6 +45,9 @@
 // The result is normalised by the per-head sum of P at the end: out = O / l, lse = m ln 2 + ln l. A row without a
 // key has l = 0 exactly; with one, l is about 1 or more, or NaN (a logit that is not finite), which goes into out and lse.
 // Every wait on the tensor cores is bounded; one that runs out sets CSA2_DEV_TIMEOUT.
+#include <atomic>
+
+#include "attend_plan.h"
 #include "csa2_internal.cuh"
 #include "tc.cuh"
 
@@ -582,35 +585,52 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attend_kernel(LatentAttend
 
 size_t latent_attend_smem_bytes() { return kSmem; }
 
-template <bool PAGED>
-static cudaError_t launch_rows(const LatentAttendArgs& a, int split, cudaStream_t s) {
-    auto k = latent_attend_kernel<PAGED>;
+cudaError_t launch_latent_attend(const LatentAttendArgs& a, cudaStream_t s) {
+    auto k = latent_attend_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     if (a.rows == 0) return cudaSuccess;
-    if (split == 1) return launch_after_prior(k, dim3((unsigned)a.rows), dim3(kThreads), kSmem, s, a);
-    if (split > 8) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    return launch_cluster(k, dim3((unsigned)(a.rows * split)), dim3(kThreads), split, kSmem, s, a);
+    return launch_after_prior(k, dim3((unsigned)a.rows), dim3(kThreads), kSmem, s, a);
 }
 
-cudaError_t launch_latent_attend(const LatentAttendArgs& a, cudaStream_t s) { return launch_rows<false>(a, 1, s); }
+// Clusters of `size` CTAs of the paged kernel that the current device (number dev) holds at once; asked once a device and
+// size. Which sizes there are and how many fit is a matter of the SMs per GPC: 7 of 16, 15 of 8, 74 of 2 on a whole
+// B200, fewer on a part of one.
+static int clusters_at_once(int dev, int size) {
+    constexpr int kDevices = 64, kSizes = 17;
+    static std::atomic<int> known[kDevices][kSizes];  // 1 more than the number; 0: not asked yet
+    if (dev >= 0 && dev < kDevices)
+        if (const int n = known[dev][size].load(std::memory_order_relaxed)) return n - 1;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, latent_attend_kernel<true>, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // (a size that the device does not take)
+        n = 0;
+    }
+    if (dev >= 0 && dev < kDevices) known[dev][size].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
 
 cudaError_t launch_paged_attend(LatentAttendArgs a, cudaStream_t s) {
-    // A tile takes about 3.5 us, what surrounds them 11 and the join 2: a row's tiles go over as many CTAs
-    // as leave every row's cluster on the GPU at once. How many of a size fit next to one another is a
-    // matter of the SMs per GPC (a second round of clusters costs more than the split gains).
-    constexpr struct { int size, rows; } kFit[] = {{16, 6}, {8, 14}, {6, 20}, {5, 24}, {4, 30}, {3, 42}, {2, 72}};
+    auto k = latent_attend_kernel<true>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     const int tiles = (a.k + kTile - 1) / kTile + (a.win > 0 ? 1 : 0);
-    a.split = 1;
-    for (const auto& f : kFit)
-        if (a.rows <= f.rows) {
-            a.split = f.size < tiles ? f.size : (tiles > 1 ? tiles : 1);
-            const int each = (tiles + a.split - 1) / a.split;
-            if (tiles > 0) a.split = (tiles + each - 1) / each;  // no smaller cluster has as few tiles per CTA
-            break;
-        }
-    return launch_rows<true>(a, a.split, s);
+    a.split = paged_attend_split(a.rows, tiles, [&](int size) { return clusters_at_once(dev, size); });
+    if (a.split == 1) return launch_after_prior(k, dim3((unsigned)a.rows), dim3(kThreads), kSmem, s, a);
+    return launch_cluster(k, dim3((unsigned)(a.rows * a.split)), dim3(kThreads), a.split, kSmem, s, a);
 }
 
 }  // namespace csa2

@@ -1,10 +1,12 @@
 """csa2_paged_attend where rows are few (a row's tiles over a cluster) and many (one CTA a row): values that are not
-finite."""
+finite, and every size of cluster. Against the formula in 64 bits, tolerance as in test_gpu_paged.py: probabilities in
+fp16 (2^-11) and fp32 terms (2^-12) of the largest key value; lse 2^-12."""
 import math
 
 import pytest
 import torch
 
+import _layer_ref as R
 import compressed_sparse_attention_append_b200 as csa
 
 pytestmark = pytest.mark.gpu
@@ -88,3 +90,32 @@ def test_nan_in_a_key_that_counts_reaches_its_row_alone(B):
         got = _attend(c, qp, q, idx, k, swa_begin=begin)
         assert all(bool(torch.isnan(x[0]).all()) for x in got)
         assert all(torch.equal(a[1:], b[1:]) for a, b in zip(got, masked))
+
+
+# rows, selected entries, window: clusters of 2 .. 16 CTAs on a whole B200 (test_attend_plan.py), one tile a CTA and several
+CLUSTERS = [(1, 128 * t - t % 3, 0) for t in range(1, 17)] + [(2, 2048, 0), (7, 2048, 0), (6, 1793, 128), (1, 2048, 128),
+            (8, 2048, 0), (20, 1000, 128), (24, 600, 0), (30, 500, 100), (42, 300, 128), (70, 640, 64), (76, 256, 128)]
+
+
+@pytest.mark.parametrize("B,k,win", CLUSTERS)
+def test_every_size_of_cluster(B, k, win):
+    n = 2500
+    c, q, qp = _case(B, n, seed=k + B)
+    idx = _select(B, n, k, seed=k)
+    idx[B // 2, k // 3:k // 2] = -1  # a gap
+    if B > 1:
+        idx[1, 128:] = -1            # CTAs without a key
+    got = _attend(c, qp, q, idx, k, win=win)
+    for r in range(B) if B < 9 else (0, 1, B // 2, B - 1):
+        e = idx[r][idx[r] >= 0].long()
+        page = c.table[r, e // c.page].long()
+        keys = R.e2m1_values(c.l_data[page, e % c.page], c.l_scale[page, e % c.page])
+        w = torch.arange(n - win, n, device=DEV)
+        keys = torch.cat([keys, c.swa[r, w % 128].cpu().view(torch.float8_e4m3fn).double()])
+        want, lse = R.attend(q[r].cpu().double(), keys, 512 ** -0.5)
+        tol = float(keys.abs().max()) * (2.0 ** -11 + 2.0 ** -12)
+        assert float((got[1][r].cpu().double() - want).abs().max()) <= tol
+        assert float((got[2][r].cpu().double() - lse).abs().max()) <= 2.0 ** -12 * max(1.0, float(lse.abs().max()))
+        assert torch.equal(got[0][r], got[1][r].to(torch.bfloat16))
+    again = _attend(c, qp, q, idx, k, win=win)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
