@@ -66,3 +66,37 @@ def test_rotations_and_workspaces_of_another_device_are_refused(path):
     csa.csa2_paged_append(cache, 1, 1, pos[:1], row, ws=Ws(buf))
     with pytest.raises(AssertionError, match="workspace of the current device"):
         csa.csa2_paged_append(cache, 1, 1, pos[:1], row, ws=Ws(buf.as_subclass(Foreign)))
+
+
+def _spoiled(t):
+    yield "type", t.double() if t.dtype is not torch.float64 else t.float()
+    yield "device", t.cpu()
+    yield "subset", t[:0] if t.shape[0] else t.unsqueeze(0)
+    yield "dimension", t.unsqueeze(0)
+    yield "rows", torch.cat([t.view(torch.uint8)] * 2).view(t.dtype)
+    if t.shape[-1] > 1:
+        yield "strides", torch.stack([t.view(torch.uint8).view(t.shape + (-1,))] * 2, -2).view(t.dtype).squeeze(-1)[..., 0]
+
+
+def test_every_tensor_of_every_call_is_checked(path):
+    """One tensor of a good call at a time: of another type, on the host, of another shape, not dense along its last axis."""
+    import test_marshal
+
+    for fn, args, kw, _, outs in test_marshal._calls():
+        for where in [*range(len(args)), *kw]:
+            t = args[where] if isinstance(where, int) else kw[where]
+            if not isinstance(t, torch.Tensor):
+                continue
+            for what, bad in _spoiled(t):
+                a, k = list(args), dict(kw)
+                if isinstance(where, int):
+                    a[where] = bad
+                else:
+                    k[where] = bad
+                torch.cuda.synchronize()
+                before = [o.clone() for o in outs]
+                with pytest.raises((AssertionError, AttributeError, ValueError, csa.Csa2Error)):
+                    fn(*a, **k)
+                    pytest.fail(f"{fn.__name__}: argument {where} with another {what} was taken")
+                torch.cuda.synchronize()
+                assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(before, outs))
