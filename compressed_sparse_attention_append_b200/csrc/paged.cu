@@ -30,7 +30,10 @@ namespace csa2 {
 namespace {
 
 constexpr int kWarps = 4;    // per block
-constexpr int kBlocks = 10;  // per SM (registers): a row is a chain of loads, so many rows at once
+// Blocks per SM (registers): a row is a chain of loads, so many rows at once, though at 48 registers the rare 64-bit
+// calls spill 96 bytes. 16 sequences of 2048 tokens with their read-back: 42 us at 6 blocks (79 registers, no spill), 40.2
+// at 8, 39.3 at 10, 38.5 at 12 (284 bytes spilled), each to 1.5 us; single tokens are the same at all.
+constexpr int kBlocks = 10;
 
 // Rounding to odd: the fp32 value next to v towards zero, its last bit set unless it is v. A further
 // rounding to a format of at most 22 bits then decides as it would for v.
