@@ -221,6 +221,7 @@ CSA2_API csa2_status csa2_paged_gather(const csa2_paged_cache* cache, int batch,
  * csa2_latent_attend over the pages: the same arguments, outputs and precision; an entry whose page
  * is not there sets CSA2_DEV_BAD_PAGE and is skipped (as is a window whose ring is not there). k >= 0:
  * k == 0 attends to the window alone (idx may then be NULL).
+ * A head with a logit that is not finite gives NaN in out and lse.
  */
 CSA2_API csa2_status csa2_paged_attend(const csa2_paged_cache* cache, int batch, int tq, const int64_t* qpos,
                                        const uint16_t* q, const int32_t* idx, int k, const int64_t* swa_begin, int win,
